@@ -53,6 +53,12 @@ typedef enum moe_dtype {
   MOE_E4M3 = 2
 } moe_dtype;
 
+/* How moe_route_scored turns logits into scores. */
+typedef enum moe_score {
+  MOE_SCORE_SIGMOID = 0,   /* s_i = 1 / (1 + e^-x_i)            */
+  MOE_SCORE_SOFTMAX = 1    /* s_i = e^x_i / sum_j e^x_j over all experts */
+} moe_score;
+
 /* Version of this ABI (increments on any signature change). */
 int moe_abi_version(void);
 
@@ -121,6 +127,74 @@ moe_status moe_route_grouped(const void* u, const void* E, moe_dtype dt, const f
                              int T, int d, int N_r, int K, int n_groups, int topk_groups,
                              int32_t* topk_idx, float* topk_gate, int32_t* counts,
                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_route_scored - the router with its choices open: x = u E^T,
+ *   s = score(x) (sigmoid, or softmax over all N_r experts)
+ *   key_i = s_i (rounded once to float32) + b_i
+ *   a group's score is the sum of its group_top largest keys; each token may
+ *   only select experts of its topk_groups best groups
+ *   the K largest keys are selected, largest first
+ *   topk_gate = gate_scale * s_k              (renorm == 0)
+ *             = gate_scale * s_k / sum_j s_j  (renorm != 0, over the selected)
+ * Equal keys and equal group scores keep the lower index.  The selection is
+ * that of exact logits: float32 inputs, and few tokens, go through float64
+ * logits; otherwise every token with a decision closer than the float32 error
+ * is selected again from float64 logits.  Renormalised gates are formed
+ * relative to the largest selected score, so they stay finite where every
+ * selected score underflows.  b_i = -inf keeps expert i out unless the kept
+ * groups hold fewer than K others; a NaN key comes before every number.
+ *   u, E, dt, T, d, N_r, K, topk_idx, topk_gate, counts, stream: as moe_route
+ *                (u and E 16-byte aligned)
+ *   b            [N_r]      device, float32, or NULL: no bias
+ *   score        a moe_score
+ *   n_groups     1..32, dividing N_r; topk_groups 1..n_groups with
+ *                topk_groups * N_r/n_groups >= K
+ *   group_top    1 or 2 (2: a group holds at least two experts)
+ *   gate_scale   finite
+ *   logits       [T, N_r]   device, float32 out, or NULL: x, for
+ *                moe_balance_loss and moe_route_scored_backward
+ *   workspace    device, >= moe_route_scored_workspace_size(T, d, N_r) bytes,
+ *                256-byte aligned; nothing in it outlives the call
+ * ------------------------------------------------------------------------ */
+size_t moe_route_scored_workspace_size(int T, int d, int N_r);
+moe_status moe_route_scored(const void* u, const void* E, moe_dtype dt, const float* b, int T,
+                            int d, int N_r, int K, moe_score score, int n_groups,
+                            int topk_groups, int group_top, int renorm, float gate_scale,
+                            int32_t* topk_idx, float* topk_gate, int32_t* counts, float* logits,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_balance_loss - the sequence-wise balance loss (the pages name it with
+ * its weight alpha; this is its usual formula).  With s' = s / sum_j s_j and
+ * a sequence of n tokens,
+ *   f_i = N_r / (K n) * number of its (token, slot) pairs routed to i
+ *   P_i = 1/n * sum of its tokens' s'_i
+ *   loss = alpha * sum_i f_i P_i
+ *   coef_i = alpha * f_i / n = dloss / ds'_{t,i}  (the selection held fixed)
+ *   logits      [T, N_r]      device, float32, from moe_route_scored
+ *   topk_idx    [T, K]        device, int32 (an id outside [0, N_r) counts for
+ *                             no expert)
+ *   seq_offsets [n_seq+1]     device, int32, non-decreasing: sequence q is
+ *                             tokens [seq_offsets[q], seq_offsets[q+1]); NULL:
+ *                             one sequence of all T (n_seq == 1).  Tokens
+ *                             outside every sequence take no part.  Values
+ *                             outside [0, T] or decreasing are clamped on the
+ *                             device (nothing outside the buffers is touched,
+ *                             the results are unspecified) and
+ *                             moe_device_status() reports bit 16
+ *   loss        [n_seq]       device, float32 out (0 for an empty sequence)
+ *   coef        [n_seq, N_r]  device, float32 out (0 for an empty sequence)
+ *   workspace   device, >= moe_balance_loss_workspace_size(T, N_r, n_seq)
+ *               bytes, 256-byte aligned
+ * Sums run in a fixed order: equal inputs give equal bits.
+ * Requires 1 <= K <= N_r <= 1024, 1 <= n_seq <= 2^20.
+ * ------------------------------------------------------------------------ */
+size_t moe_balance_loss_workspace_size(int T, int N_r, int n_seq);
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx,
+                            const int32_t* seq_offsets, int n_seq, int T, int N_r, int K,
+                            moe_score score, float alpha, float* loss, float* coef,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * moe_permute - group the T*K (token, slot) pairs by expert and copy the
@@ -452,6 +526,71 @@ moe_status moe_unpermute_backward(const void* dh_out, const void* dx_shared, int
 moe_status moe_router_weight_grad(const void* x, const int32_t* x_rows,
                                   const float* d_logit_perm, const int32_t* offsets,
                                   moe_dtype dt, int N_r, int d, float* dE, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_route_scored_backward - gradients of moe_route_scored and of
+ * moe_balance_loss, the selection held fixed, for upstream d_gate and d_loss:
+ *   d_logit = gradient of  sum_{t,k} d_gate[t,k] topk_gate[t,k]
+ *                        + sum_q d_loss[q] loss[q]   with respect to x
+ *   du[t]   = du_base[t] + sum_i d_logit[t,i] E[i]
+ *   dE[i]   = sum_t d_logit[t,i] u[t]
+ *   u, E, dt, T, d, N_r, K, score, renorm, gate_scale: as in the forward
+ *   logits      [T, N_r]   device, float32, from moe_route_scored
+ *   topk_idx    [T, K]     device, int32 (a slot whose id lies outside
+ *                          [0, N_r) is left out of the selection)
+ *   d_gate      [T, K]     device, float32, or NULL: no gate gradient (e.g.
+ *                          from moe_combine_backward)
+ *   seq_offsets, n_seq     as moe_balance_loss
+ *   balance_coef [n_seq, N_r] device, float32, from moe_balance_loss, or NULL:
+ *                          no balance gradient (d_gate or balance_coef is given)
+ *   d_loss      [n_seq]    device, float32, or NULL: 1 for every sequence
+ *   du_base     [T, d]     device, dt, or NULL: zero; may be du itself
+ *   d_logit     [T, N_r]   device, float32 out, or NULL: not wanted
+ *   du          [T, d]     device, dt out;  dE [N_r, d] device, float32 out
+ *   workspace   device, >= moe_route_scored_backward_workspace_size(dt, T, d,
+ *               N_r) bytes, 256-byte aligned
+ * Sums run in a fixed order; du is rounded once to dt.  Same size limits as
+ * moe_route_scored; u, E, du and dE 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+size_t moe_route_scored_backward_workspace_size(moe_dtype dt, int T, int d, int N_r);
+moe_status moe_route_scored_backward(const void* u, const void* E, moe_dtype dt,
+                                     const float* logits, const int32_t* topk_idx,
+                                     const float* d_gate, const int32_t* seq_offsets, int n_seq,
+                                     const float* balance_coef, const float* d_loss, int T, int d,
+                                     int N_r, int K, moe_score score, int renorm,
+                                     float gate_scale, const void* du_base, float* d_logit,
+                                     void* du, float* dE, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_expert_gate_up_save8 / moe_expert_ffn_backward8 - the training FFN with
+ * its activation checkpoint in 8 bits: instead of moe_expert_gate_up_save's
+ * a_gu (bf16) and h, 6 I bytes a row, the backward keeps 2 I bytes and the
+ * scales.  With a = x W_gate_up[g]^T (float32), per row and 128 columns,
+ *   a_scale = amax/448 (1 if all zero),  a_q = E4M3_rne_satfinite(a / a_scale)
+ * (IEEE float32 division), and the backward works from a' = a_q * a_scale:
+ *   h' = SiLU(a'_gate) * a'_up (bf16; for dW_down)
+ *   dA = [dh * a'_up * SiLU'(a'_gate) | dh * SiLU(a'_gate)],  dh = dy W_down[g]
+ *   dx, dW_down = sum dy^T h', dW_gate_up as moe_expert_ffn_backward.
+ * MOE_BF16 only.  h [rows, I] is moe_expert_gate_up's, bit for bit, for the
+ * down projection; it need not be kept for the backward.
+ *   a_q [rows, 2I] device e4m3 (gate columns first), 16-byte aligned;
+ *   a_scale [rows, 2I/128] device float32; the other arguments as
+ *   moe_expert_gate_up_save / moe_expert_ffn_backward.  Rows outside every
+ *   group are not written.  gate_up_save8: d % 128 == 0, I % 128 == 0;
+ *   backward8: d % 256 == 0, I % 256 == 0, workspace of
+ *   moe_expert_ffn_backward8_workspace_size bytes, 256-byte aligned.
+ * ------------------------------------------------------------------------ */
+moe_status moe_expert_gate_up_save8(const void* x, const int32_t* offsets, int n_groups, int rows,
+                                    int d, int I, moe_dtype dt, const void* W_gate_up, void* h,
+                                    uint8_t* a_q, float* a_scale, void* stream);
+size_t moe_expert_ffn_backward8_workspace_size(moe_dtype dt, int rows, int d, int I,
+                                               int n_groups);
+moe_status moe_expert_ffn_backward8(const void* x, const int32_t* offsets, int n_groups, int rows,
+                                    int d, int I, moe_dtype dt, const void* W_gate_up,
+                                    const void* W_down, const uint8_t* a_q, const float* a_scale,
+                                    const void* dy, void* dx, void* dW_gate_up, void* dW_down,
+                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* ========================================================================
  * Expert parallelism ("DeepSeek V3 & R1 論文研究", sections DeepSeekMoE and

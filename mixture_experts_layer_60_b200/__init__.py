@@ -24,6 +24,12 @@ __all__ = [
     "moe_expert_ffn_backward_workspace_size", "moe_unpermute_backward", "moe_router_weight_grad",
     "moe_quantize_128x1_grouped", "moe_ep_plan", "moe_ep_dispatch", "moe_ep_return",
     "moe_permute_index",
+    "MOE_SCORE_SIGMOID", "MOE_SCORE_SOFTMAX",
+    "moe_route_scored", "moe_route_scored_workspace_size",
+    "moe_balance_loss", "moe_balance_loss_workspace_size",
+    "moe_route_scored_backward", "moe_route_scored_backward_workspace_size",
+    "moe_expert_gate_up_save8", "moe_expert_ffn_backward8",
+    "moe_expert_ffn_backward8_workspace_size",
 ]
 
 # MOE_LIBRARY (environment) selects another build of the library, e.g. the
@@ -32,6 +38,7 @@ LIB_PATH = os.environ.get("MOE_LIBRARY") or os.path.join(os.path.dirname(os.path
                                                          "libmoe.so")
 
 MOE_F32, MOE_BF16, MOE_E4M3 = 0, 1, 2
+MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
           4: "MOE_ERR_CUDA", 5: "MOE_ERR_TIMEOUT"}
 
@@ -75,6 +82,18 @@ SYMBOLS = {
                                     _vp]),
     "moe_router_weight_grad": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
     "moe_quantize_128x1_grouped": (_i, [_vp, _i, _i, _vp, _i, _vp, _vp, _vp, _vp]),
+    "moe_route_scored_workspace_size": (_sz, [_i, _i, _i]),
+    "moe_route_scored": (_i, [_vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp,
+                              _vp, _vp, _vp, _sz, _vp]),
+    "moe_balance_loss_workspace_size": (_sz, [_i, _i, _i]),
+    "moe_balance_loss": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _sz, _vp]),
+    "moe_route_scored_backward_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "moe_route_scored_backward": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i,
+                                       _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_expert_gate_up_save8": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
+    "moe_expert_ffn_backward8_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "moe_expert_ffn_backward8": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp,
+                                      _vp, _vp, _vp, _sz, _vp]),
     "moe_ep_plan": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp]),
     "moe_ep_dispatch": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _i,
                              ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.c_longlong, _vp]),
@@ -367,6 +386,148 @@ def moe_quantize_128x1_grouped(x, offsets, q, scale, block_start, stream=None):
     n_groups = 1 if offsets is None else offsets.shape[0] - 1
     _check(lib().moe_quantize_128x1_grouped(_p(x), rows, cols, _p(offsets), n_groups, _p(q),
                                             _p(scale), _p(block_start), _s(stream)))
+
+
+# ------------------------------------------------------------------ scored router
+
+_I32, _F32 = torch.int32, torch.float32
+
+
+def _want(who, **tensors):
+    """Refuses a tensor of another type or shape than the call reads or writes: name=(tensor,
+    dtype or dtypes, shape); a tensor of None is left to the library's own check."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype and (type(dtype) is not tuple or t.dtype not in dtype):
+            raise ValueError(f"{who}: {name} is {t.dtype}, not {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{who}: {name} has shape {tuple(t.shape)}, not {shape}")
+
+
+def _here(who, t):
+    """The library launches on the current device: its tensors have to live there."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{who}: tensors are on {t.device}, not on the current device")
+
+
+def moe_route_scored_workspace_size(T: int, d: int, N_r: int) -> int:
+    return lib().moe_route_scored_workspace_size(T, d, N_r)
+
+
+def moe_route_scored(u, E, b, K, topk_idx, topk_gate, counts, workspace,
+                     score=MOE_SCORE_SIGMOID, n_groups=1, topk_groups=1, group_top=1, renorm=True,
+                     gate_scale=1.0, logits=None, stream=None):
+    """The router with softmax or sigmoid scores, group scores of one or two keys, raw or
+    renormalised gates; `logits` [T, N_r] float32 keeps the logits for the backward.  b may be
+    None."""
+    who = "moe_route_scored"
+    T, d = u.shape
+    N_r = E.shape[0]
+    _here(who, u)
+    _want(who, E=(E, u.dtype, (N_r, d)), b=(b, _F32, (N_r,)), topk_idx=(topk_idx, _I32, (T, K)),
+          topk_gate=(topk_gate, _F32, (T, K)), counts=(counts, _I32, (N_r,)),
+          logits=(logits, _F32, (T, N_r)))
+    _check(lib().moe_route_scored(_p(u), _p(E), _dt(u), _p(b), T, d, N_r, K, score, n_groups,
+                                  topk_groups, group_top, 1 if renorm else 0, gate_scale,
+                                  _p(topk_idx), _p(topk_gate), _p(counts), _p(logits),
+                                  _p(workspace), _nbytes(workspace), _s(stream)))
+
+
+def moe_balance_loss_workspace_size(T: int, N_r: int, n_seq: int) -> int:
+    return lib().moe_balance_loss_workspace_size(T, N_r, n_seq)
+
+
+def moe_balance_loss(logits, topk_idx, alpha, loss, coef, workspace, score=MOE_SCORE_SIGMOID,
+                     seq_offsets=None, stream=None):
+    """The sequence-wise balance loss [n_seq] and the coefficients [n_seq, N_r] of its gradient."""
+    who = "moe_balance_loss"
+    T, N_r = logits.shape
+    n_seq = loss.shape[0]
+    K = topk_idx.shape[1]
+    _here(who, logits)
+    _want(who, logits=(logits, _F32, (T, N_r)), topk_idx=(topk_idx, _I32, (T, K)),
+          loss=(loss, _F32, (n_seq,)), coef=(coef, _F32, (n_seq, N_r)),
+          seq_offsets=(seq_offsets, _I32, (n_seq + 1,)))
+    _check(lib().moe_balance_loss(_p(logits), _p(topk_idx), _p(seq_offsets), n_seq, T, N_r, K,
+                                  score, alpha, _p(loss), _p(coef), _p(workspace),
+                                  _nbytes(workspace), _s(stream)))
+
+
+def moe_route_scored_backward_workspace_size(dt: int, T: int, d: int, N_r: int) -> int:
+    return lib().moe_route_scored_backward_workspace_size(dt, T, d, N_r)
+
+
+def moe_route_scored_backward(u, E, logits, topk_idx, d_gate, du, dE, workspace,
+                              score=MOE_SCORE_SIGMOID, renorm=True, gate_scale=1.0,
+                              seq_offsets=None, balance_coef=None, d_loss=None, du_base=None,
+                              d_logit=None, stream=None):
+    """Gradients of moe_route_scored's gates (d_gate, or None) and of moe_balance_loss
+    (balance_coef, d_loss): du = du_base + ..., dE, and the logits' own gradient d_logit where it
+    is asked for."""
+    who = "moe_route_scored_backward"
+    T, d = u.shape
+    N_r = E.shape[0]
+    K = topk_idx.shape[1]
+    n_seq = 1 if balance_coef is None else balance_coef.shape[0]
+    _here(who, u)
+    _want(who, E=(E, u.dtype, (N_r, d)), logits=(logits, _F32, (T, N_r)),
+          topk_idx=(topk_idx, _I32, (T, K)), d_gate=(d_gate, _F32, (T, K)),
+          du=(du, u.dtype, (T, d)), dE=(dE, _F32, (N_r, d)), du_base=(du_base, u.dtype, (T, d)),
+          d_logit=(d_logit, _F32, (T, N_r)), balance_coef=(balance_coef, _F32, (n_seq, N_r)),
+          d_loss=(d_loss, _F32, (n_seq,)))
+    if balance_coef is None:
+        seq_offsets = None
+    _want(who, seq_offsets=(seq_offsets, _I32, (n_seq + 1,)))
+    _check(lib().moe_route_scored_backward(
+        _p(u), _p(E), _dt(u), _p(logits), _p(topk_idx), _p(d_gate), _p(seq_offsets), n_seq,
+        _p(balance_coef), _p(d_loss), T, d, N_r, K, score, 1 if renorm else 0, gate_scale,
+        _p(du_base), _p(d_logit), _p(du), _p(dE), _p(workspace), _nbytes(workspace), _s(stream)))
+
+
+# ------------------------------------------------------------------ 8-bit checkpoints
+
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+
+
+def moe_expert_gate_up_save8(x, offsets, W_gate_up, h, a_q, a_scale, stream=None):
+    """moe_expert_gate_up that also keeps the pre-activations as E4M3 a_q [rows, 2I] with a scale
+    for each row and 128 columns, a_scale [rows, 2I/128]."""
+    who = "moe_expert_gate_up_save8"
+    rows, d = x.shape
+    n_groups, two_i, _ = W_gate_up.shape
+    _here(who, x)
+    _want(who, W_gate_up=(W_gate_up, x.dtype, (n_groups, two_i, d)),
+          offsets=(offsets, _I32, (n_groups + 1,)), h=(h, x.dtype, (rows, two_i // 2)),
+          a_q=(a_q, _E4M3, (rows, two_i)), a_scale=(a_scale, _F32, (rows, two_i // 128)))
+    _check(lib().moe_expert_gate_up_save8(_p(x), _p(offsets), n_groups, rows, d, two_i // 2,
+                                          _dt(x), _p(W_gate_up), _p(h), _p(a_q), _p(a_scale),
+                                          _s(stream)))
+
+
+def moe_expert_ffn_backward8_workspace_size(dt: int, rows: int, d: int, I: int,
+                                            n_groups: int) -> int:
+    return lib().moe_expert_ffn_backward8_workspace_size(dt, rows, d, I, n_groups)
+
+
+def moe_expert_ffn_backward8(x, offsets, W_gate_up, W_down, a_q, a_scale, dy, dx, dW_gate_up,
+                             dW_down, workspace, stream=None):
+    """moe_expert_ffn_backward from the checkpoint of moe_expert_gate_up_save8."""
+    who = "moe_expert_ffn_backward8"
+    rows, d = dy.shape
+    n_groups, two_i, _ = W_gate_up.shape
+    _here(who, x)
+    t = x.dtype
+    _want(who, x=(x, t, (rows, d)), W_gate_up=(W_gate_up, t, (n_groups, two_i, d)),
+          W_down=(W_down, t, (n_groups, d, two_i // 2)), offsets=(offsets, _I32, (n_groups + 1,)),
+          a_q=(a_q, _E4M3, (rows, two_i)), a_scale=(a_scale, _F32, (rows, two_i // 128)),
+          dy=(dy, t, (rows, d)), dx=(dx, t, (rows, d)),
+          dW_gate_up=(dW_gate_up, t, (n_groups, two_i, d)),
+          dW_down=(dW_down, t, (n_groups, d, two_i // 2)))
+    _check(lib().moe_expert_ffn_backward8(
+        _p(x), _p(offsets), n_groups, rows, d, two_i // 2, _dt(x), _p(W_gate_up), _p(W_down),
+        _p(a_q), _p(a_scale), _p(dy), _p(dx), _p(dW_gate_up), _p(dW_down), _p(workspace),
+        _nbytes(workspace), _s(stream)))
 
 
 # ------------------------------------------------------------------ expert parallelism

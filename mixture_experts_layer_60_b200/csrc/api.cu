@@ -3,6 +3,7 @@
 #include "launch.h"
 
 #include <atomic>
+#include <cmath>
 
 using namespace moe;
 
@@ -185,6 +186,115 @@ moe_status moe_route_grouped(const void* u, const void* E, moe_dtype dt, const f
                              void* workspace, size_t workspace_bytes, void* stream) {
   return route_impl("moe_route_grouped", u, E, dt, b, T, d, N_r, K, n_groups, topk_groups,
                     topk_idx, topk_gate, counts, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Size checks shared by the scored router's forward, backward and balance loss.
+moe_status check_scored(const char* who, int T, int N_r, int K, int score) {
+  MOE_REQUIRE(T >= 0 && N_r > 0 && K > 0, MOE_ERR_INVALID_ARG, "%s: bad sizes T=%d N_r=%d K=%d",
+              who, T, N_r, K);
+  MOE_REQUIRE(N_r <= 1024 && K <= N_r, MOE_ERR_UNSUPPORTED,
+              "%s: need 1 <= K <= N_r <= 1024 (K=%d N_r=%d)", who, K, N_r);
+  MOE_REQUIRE((long long)T * N_r <= 0x7fffffffLL, MOE_ERR_UNSUPPORTED,
+              "%s: T * N_r must fit in 31 bits (T=%d N_r=%d)", who, T, N_r);
+  MOE_REQUIRE(score == MOE_SCORE_SIGMOID || score == MOE_SCORE_SOFTMAX, MOE_ERR_INVALID_ARG,
+              "%s: unknown score %d", who, score);
+  return MOE_OK;
+}
+
+moe_status check_scored_row(const char* who, moe_dtype dt, int d) {
+  MOE_REQUIRE(dt == MOE_F32 || dt == MOE_BF16, MOE_ERR_UNSUPPORTED,
+              "%s: dtype must be MOE_F32 or MOE_BF16", who);
+  MOE_REQUIRE(d > 0, MOE_ERR_INVALID_ARG, "%s: bad size d=%d", who, d);
+  MOE_REQUIRE(d % 64 == 0, MOE_ERR_UNSUPPORTED, "%s: d=%d must be a multiple of 64", who, d);
+  MOE_REQUIRE((long long)d * dtype_bytes(dt) <= 32768, MOE_ERR_UNSUPPORTED,
+              "%s: a row of u is at most 32 KB (d=%d)", who, d);
+  return MOE_OK;
+}
+
+moe_status check_workspace(const char* who, const void* ws, size_t have, size_t need) {
+  MOE_REQUIRE(need == 0 || ws, MOE_ERR_INVALID_ARG, "%s: null workspace", who);
+  MOE_REQUIRE(have >= need, MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", who, have, need);
+  MOE_REQUIRE(reinterpret_cast<uintptr_t>(ws) % 256 == 0, MOE_ERR_INVALID_ARG,
+              "%s: workspace must be 256-byte aligned", who);
+  return MOE_OK;
+}
+
+moe_status check_sequences(const char* who, const int32_t* seq_offsets, int n_seq) {
+  MOE_REQUIRE(n_seq >= 1 && n_seq <= 1 << 20, MOE_ERR_INVALID_ARG, "%s: n_seq=%d (1..2^20)", who,
+              n_seq);
+  MOE_REQUIRE(seq_offsets || n_seq == 1, MOE_ERR_INVALID_ARG,
+              "%s: n_seq=%d sequences need seq_offsets", who, n_seq);
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_route_scored_workspace_size(int T, int d, int N_r) {
+  if (T <= 0 || d <= 0 || N_r <= 0) return 0;
+  return route_scored_ws_bytes(T, d, N_r);
+}
+
+moe_status moe_route_scored(const void* u, const void* E, moe_dtype dt, const float* b, int T,
+                            int d, int N_r, int K, moe_score score, int n_groups,
+                            int topk_groups, int group_top, int renorm, float gate_scale,
+                            int32_t* topk_idx, float* topk_gate, int32_t* counts, float* logits,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  clear_last_error();
+  const char* who = "moe_route_scored";
+  MOE_TRY(check_scored(who, T, N_r, K, (int)score));
+  MOE_TRY(check_scored_row(who, dt, d));
+  MOE_REQUIRE(n_groups >= 1 && n_groups <= 32 && N_r % n_groups == 0 && topk_groups >= 1 &&
+                  topk_groups <= n_groups,
+              MOE_ERR_INVALID_ARG,
+              "%s: need 1 <= topk_groups <= n_groups <= 32 with N_r %% n_groups == 0", who);
+  MOE_REQUIRE((long long)topk_groups * (N_r / n_groups) >= K, MOE_ERR_INVALID_ARG,
+              "%s: the kept groups hold fewer than K experts", who);
+  MOE_REQUIRE(group_top == 1 || (group_top == 2 && (N_r / n_groups >= 2 || n_groups == 1)),
+              MOE_ERR_INVALID_ARG, "%s: group_top=%d must be 1, or 2 with two experts a group",
+              who, group_top);
+  MOE_REQUIRE(std::isfinite(gate_scale), MOE_ERR_INVALID_ARG, "%s: gate_scale is not finite", who);
+  MOE_REQUIRE(E && counts, MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+  MOE_REQUIRE(T == 0 || (u && topk_idx && topk_gate), MOE_ERR_INVALID_ARG, "%s: null pointer",
+              who);
+  MOE_REQUIRE(al16(u) && al16(E), MOE_ERR_INVALID_ARG, "%s: u and E must be 16-byte aligned", who);
+  MOE_TRY(check_workspace(who, workspace, workspace_bytes,
+                          moe_route_scored_workspace_size(T, d, N_r)));
+  MOE_TRY(check_device());
+  cudaStream_t s = as_stream(stream);
+  if (T == 0)
+    return cuda_check(cudaMemsetAsync(counts, 0, (size_t)N_r * sizeof(int32_t), s), "zero counts");
+  return launch_route_scored(u, E, dt, b, T, d, N_r, K, (int)score, n_groups, topk_groups,
+                             group_top, renorm != 0, gate_scale, topk_idx, topk_gate, counts,
+                             logits, workspace, s);
+}
+
+size_t moe_balance_loss_workspace_size(int T, int N_r, int n_seq) {
+  if (T < 0 || N_r <= 0 || n_seq <= 0) return 0;
+  return balance_ws_bytes(T, N_r, n_seq);
+}
+
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx,
+                            const int32_t* seq_offsets, int n_seq, int T, int N_r, int K,
+                            moe_score score, float alpha, float* loss, float* coef,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  clear_last_error();
+  const char* who = "moe_balance_loss";
+  MOE_TRY(check_scored(who, T, N_r, K, (int)score));
+  MOE_TRY(check_sequences(who, seq_offsets, n_seq));
+  MOE_REQUIRE(std::isfinite(alpha), MOE_ERR_INVALID_ARG, "%s: alpha is not finite", who);
+  MOE_REQUIRE(loss && coef, MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+  MOE_REQUIRE(T == 0 || (logits && topk_idx), MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+  MOE_TRY(check_workspace(who, workspace, workspace_bytes,
+                          moe_balance_loss_workspace_size(T, N_r, n_seq)));
+  MOE_TRY(check_device());
+  return launch_balance_loss(logits, topk_idx, seq_offsets, n_seq, T, N_r, K, (int)score, alpha,
+                             loss, coef, workspace, as_stream(stream));
 }
 
 size_t moe_permute_workspace_size(int T, int N_r) {
@@ -767,6 +877,118 @@ moe_status moe_router_weight_grad(const void* x_perm, const int32_t* x_rows,
   MOE_TRY(check_device());
   return launch_router_weight_grad(x_perm, x_rows, d_logit_perm, offsets, dt, N_r, d, dE,
                                    as_stream(stream));
+}
+
+size_t moe_route_scored_backward_workspace_size(moe_dtype dt, int T, int d, int N_r) {
+  if (T <= 0 || d <= 0 || N_r <= 0) return 0;
+  return route_scored_bwd_ws_bytes(dt, T, d, N_r);
+}
+
+moe_status moe_route_scored_backward(const void* u, const void* E, moe_dtype dt,
+                                     const float* logits, const int32_t* topk_idx,
+                                     const float* d_gate, const int32_t* seq_offsets, int n_seq,
+                                     const float* balance_coef, const float* d_loss, int T, int d,
+                                     int N_r, int K, moe_score score, int renorm,
+                                     float gate_scale, const void* du_base, float* d_logit,
+                                     void* du, float* dE, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  clear_last_error();
+  const char* who = "moe_route_scored_backward";
+  MOE_TRY(check_scored(who, T, N_r, K, (int)score));
+  MOE_TRY(check_scored_row(who, dt, d));
+  MOE_TRY(check_sequences(who, seq_offsets, n_seq));
+  MOE_REQUIRE(std::isfinite(gate_scale), MOE_ERR_INVALID_ARG, "%s: gate_scale is not finite", who);
+  MOE_REQUIRE(T == 0 || d_gate || balance_coef, MOE_ERR_INVALID_ARG,
+              "%s: neither d_gate nor balance_coef is given", who);
+  MOE_REQUIRE(balance_coef || !d_loss, MOE_ERR_INVALID_ARG, "%s: d_loss without balance_coef", who);
+  MOE_REQUIRE(E && dE, MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+  MOE_REQUIRE(T == 0 || (u && logits && topk_idx && du), MOE_ERR_INVALID_ARG, "%s: null pointer",
+              who);
+  MOE_REQUIRE(al16(u) && al16(E) && al16(du_base) && al16(du) && al16(dE), MOE_ERR_INVALID_ARG,
+              "%s: u, E, du_base, du and dE must be 16-byte aligned", who);
+  MOE_TRY(check_workspace(who, workspace, workspace_bytes,
+                          moe_route_scored_backward_workspace_size(dt, T, d, N_r)));
+  MOE_TRY(check_device());
+  cudaStream_t s = as_stream(stream);
+  if (T == 0)
+    return cuda_check(cudaMemsetAsync(dE, 0, (size_t)N_r * d * sizeof(float), s), "zero dE");
+  return launch_route_scored_backward(u, E, dt, logits, topk_idx, d_gate, seq_offsets, n_seq,
+                                      balance_coef, d_loss, T, d, N_r, K, (int)score, renorm != 0,
+                                      gate_scale, du_base, d_logit, du, dE, workspace, s);
+}
+
+// ---------------------------------------------------------------- 8-bit checkpoints
+
+moe_status moe_expert_gate_up_save8(const void* x, const int32_t* offsets, int n_groups, int rows,
+                                    int d, int I, moe_dtype dt, const void* W_gate_up, void* h,
+                                    uint8_t* a_q, float* a_scale, void* stream) {
+  clear_last_error();
+  const char* who = "moe_expert_gate_up_save8";
+  MOE_TRY(check_ffn_common(who, x, offsets, n_groups, rows, d, I, dt, W_gate_up));
+  MOE_REQUIRE(dt == MOE_BF16, MOE_ERR_UNSUPPORTED, "%s: MOE_BF16 only", who);
+  if (rows == 0) return MOE_OK;
+  MOE_REQUIRE(h && a_q && a_scale, MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+  MOE_REQUIRE(al16(x) && al16(W_gate_up) && al16(h) && al16(a_q), MOE_ERR_INVALID_ARG,
+              "%s: x, W_gate_up, h and a_q must be 16-byte aligned", who);
+  MOE_TRY(check_device());
+  return launch_ws_gate_up_save8(x, W_gate_up, offsets, n_groups, rows, I, d, h, a_q, a_scale,
+                                 as_stream(stream));
+}
+
+namespace {
+
+// Backward workspace from an 8-bit checkpoint: dA [rows, 2I] bf16, h [rows, I]
+// bf16, then the weight gradients' tail blocks.
+size_t ffn_bwd8_ws(moe_dtype dt, int rows, int d, int I, int G) {
+  if (dt != MOE_BF16 || rows <= 0 || d <= 0 || I <= 0 || G <= 0) return 0;
+  return align_up((size_t)rows * 2 * I * 2, 256) + align_up((size_t)rows * I * 2, 256) +
+         wgrad_tail_bytes((size_t)(d > 2 * I ? d : 2 * I) * 2, 64, G);
+}
+
+}  // namespace
+
+size_t moe_expert_ffn_backward8_workspace_size(moe_dtype dt, int rows, int d, int I,
+                                               int n_groups) {
+  return ffn_bwd8_ws(dt, rows, d, I, n_groups);
+}
+
+moe_status moe_expert_ffn_backward8(const void* x, const int32_t* offsets, int n_groups, int rows,
+                                    int d, int I, moe_dtype dt, const void* W_gate_up,
+                                    const void* W_down, const uint8_t* a_q, const float* a_scale,
+                                    const void* dy, void* dx, void* dW_gate_up, void* dW_down,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  clear_last_error();
+  const char* who = "moe_expert_ffn_backward8";
+  MOE_TRY(check_ffn_common(who, x, offsets, n_groups, rows, d, I, dt, W_gate_up));
+  MOE_REQUIRE(dt == MOE_BF16, MOE_ERR_UNSUPPORTED, "%s: MOE_BF16 only", who);
+  MOE_REQUIRE(d % 256 == 0 && I % 256 == 0, MOE_ERR_UNSUPPORTED,
+              "%s: d=%d and I=%d must be multiples of 256", who, d, I);
+  MOE_REQUIRE(W_down && dW_gate_up && dW_down, MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+  MOE_REQUIRE(al16(W_gate_up) && al16(W_down) && al16(dW_gate_up) && al16(dW_down),
+              MOE_ERR_INVALID_ARG, "%s: weights and their gradients must be 16-byte aligned", who);
+  cudaStream_t s = as_stream(stream);
+  if (rows == 0) {
+    MOE_TRY(check_device());
+    MOE_TRY(cuda_check(cudaMemsetAsync(dW_gate_up, 0, (size_t)n_groups * 2 * I * d * 2, s),
+                       "zero dW_gate_up"));
+    return cuda_check(cudaMemsetAsync(dW_down, 0, (size_t)n_groups * d * I * 2, s),
+                      "zero dW_down");
+  }
+  MOE_REQUIRE(a_q && a_scale && dy && dx, MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+  MOE_REQUIRE(al16(x) && al16(a_q) && al16(dy) && al16(dx), MOE_ERR_INVALID_ARG,
+              "%s: activations must be 16-byte aligned", who);
+  MOE_TRY(check_workspace(who, workspace, workspace_bytes, ffn_bwd8_ws(dt, rows, d, I, n_groups)));
+  MOE_TRY(check_device());
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  void* dA = w;
+  void* h = w + align_up((size_t)rows * 2 * I * 2, 256);
+  void* tail = static_cast<uint8_t*>(h) + align_up((size_t)rows * I * 2, 256);
+  // Dgrad of the down projection fused with the SwiGLU backward -> dA, h
+  MOE_TRY(launch_ws_dswiglu8(dy, W_down, offsets, n_groups, rows, I, d, a_q, a_scale, dA, h, s));
+  MOE_TRY(launch_wgrad_gemm(dy, d, h, I, offsets, n_groups, rows, tail, dW_down, s));
+  MOE_TRY(launch_ws_gemm_ex(dA, W_gate_up, 0, offsets, n_groups, rows, d, 2 * I, WS_STORE, true,
+                            dx, d, nullptr, 0, s));
+  return launch_wgrad_gemm(dA, 2 * I, x, d, offsets, n_groups, rows, tail, dW_gate_up, s);
 }
 
 // ---------------------------------------------------------------- expert parallelism

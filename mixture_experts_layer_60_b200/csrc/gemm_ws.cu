@@ -15,6 +15,12 @@
 // every other 32-token chunk):
 //   SWIGLU  h[tok0+j, nt*128 + n] = bf16(SiLU(D_gate[n,j]) * D_up[n,j])
 //   STORE   y[tok0+j, nt*256 + n] = bf16(D0[n,j]), y[.., nt*256+128+n] = bf16(D1[n,j])
+//   SWIGLU_SAVE8  h, and D_gate, D_up as E4M3 with a scale amax / 448 for each
+//           token and 128 columns.  A tile's columns are the lanes of four
+//           warps: each reduces its 32 over the lanes and the four exchange
+//           the maxima of a 32-token chunk through shared memory.
+//   DSWIGLU8  the SwiGLU backward from such a checkpoint; writes h again too
+//           (the down projection's weight gradient needs it).
 // Values are transposed through a 2 KB shared-memory patch per warp so that
 // global stores are 16-byte vectors along token rows.
 //
@@ -59,7 +65,12 @@ constexpr int OFF_BAR = OFF_STAGE_OUT + kEpiWarps * 2048;
 constexpr int N_BARS = 2 * STAGES + 3;
 constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
 constexpr int OFF_TAB = OFF_MISC + 16;
-constexpr int SMEM_BYTES = OFF_TAB + 2 * (kMaxGroups + 1) * 4;
+constexpr int OFF_AMAX = OFF_TAB + 2 * (kMaxGroups + 1) * 4;
+// SWIGLU_SAVE8: [2 chunk halves][2 slots][4 lane quarters][gate, up][32 tokens] maxima
+// and a barrier for each (half, slot)
+constexpr int AMAX_BYTES = 2 * 2 * 4 * 2 * 32 * 4;
+constexpr int OFF_XBAR = (OFF_AMAX + AMAX_BYTES + 7) / 8 * 8;
+constexpr int SMEM_BYTES = OFF_XBAR + 4 * 8;
 constexpr int SMEM_ALLOC = SMEM_BYTES + 1024;
 
 struct WsParams {
@@ -74,6 +85,9 @@ struct WsParams {
   int ldc;                  // row stride of C in elements
   __nv_bfloat16* S;         // SWIGLU_SAVE: pre-activations written; DSWIGLU: read
   int lds;                  // row stride of S (2I)
+  uint8_t* Q;               // *8: E4M3 pre-activations [rows, 2I]
+  float* QS;                // *8: their scales [rows, 2I/128]
+  __nv_bfloat16* H;         // DSWIGLU8: h written [rows, I]
   int n_extra;              // extra groups after the routed ones (0: none)
   int T_extra;              // rows of each extra group
   int x_extra_local;        // 1: extra groups read X rows [0, T_extra); 0: their C rows
@@ -82,7 +96,9 @@ struct WsParams {
 
 template <int EPI>
 struct TileMath {
-  static constexpr bool SW = EPI == WS_SWIGLU || EPI == WS_SWIGLU_SAVE;
+  static constexpr bool SW =
+      EPI == WS_SWIGLU || EPI == WS_SWIGLU_SAVE || EPI == WS_SWIGLU_SAVE8;
+  static constexpr bool DSW = EPI == WS_DSWIGLU || EPI == WS_DSWIGLU8;
   static constexpr int OUT_COLS = SW ? 128 : 256;   // output columns per weight tile
 };
 
@@ -137,6 +153,23 @@ __device__ __forceinline__ void raise_abort(volatile int* abort, int* err) {
   atomicOr(err, ERR_GEMM_TIMEOUT);
 }
 
+__device__ __forceinline__ float amax_scale(float amax) {
+  return amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f);
+}
+
+// Eight E4M3 bytes times a scale.
+__device__ __forceinline__ void e4m3x8(const uint2& v, float sc, float* f) {
+  const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+        (__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+    const float2 p = __half22float2(__half2(h));
+    f[2 * i] = p.x * sc;
+    f[2 * i + 1] = p.y * sc;
+  }
+}
+
 // SiLU for a bf16 result: fast exponential and division are well inside bf16 rounding.
 __device__ __forceinline__ float silu_f(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
 
@@ -164,6 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* mma_done = tempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  float* amax_x = reinterpret_cast<float*>(smem + OFF_AMAX);
+  uint64_t* xbar = reinterpret_cast<uint64_t*>(smem + OFF_XBAR);
   int* prefix = reinterpret_cast<int*>(smem + OFF_TAB);
   int* roff = prefix + kMaxGroups + 1;
 
@@ -177,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(tfull, 1);
     mbar_init(tempty, kEpiWarps);      // one arrival per epilogue warp
     mbar_init(mma_done, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 4);   // the four lane quarters' warps
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmW);
@@ -335,7 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ch = (warp - 2) >> 2;               // which alternate 32-token chunks this warp takes
     uint16_t* patch = reinterpret_cast<uint16_t*>(sOut + (warp - 2) * 2048);   // [32 tok][32 col]
     uint32_t tphase = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    uint32_t xit = 0;                             // SWIGLU_SAVE8: exchanges done
+    bool xok = true;
+    for (int t = blockIdx.x; t < total && xok; t += gridDim.x) {
       int g, nt, tok0, count, xrow0;
       decode_tile(t, prefix, roff, G, Gtot, p, g, nt, tok0, count, xrow0);
       const bool got = mbar_wait_bounded(tfull, tphase, abort_flag, kWaitNs);
@@ -346,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t tl = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
       const int nch = (count + 31) / 32;
-      if (EPI == WS_DSWIGLU) {
+      if (TileMath<EPI>::DSW) {
         // dh[tok, col] from TMEM; a = S[tok, col], b = S[tok, I + col]:
         //   dA[tok, col] = dh * b * SiLU'(a),  dA[tok, I + col] = dh * SiLU(a).
         // dh goes through a float32 [16 tok][32 col] patch so that every
@@ -367,6 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
               // both 16-byte pieces of this lane first, then the arithmetic
               uint4 av[2], bv[2];
+              uint2 aq[2], bq[2];
+              float as[2], bs[2];
               size_t grow[2];
               int col[2], c8[2], row[2];
               bool ok[2];
@@ -381,8 +421,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 grow[it] = (size_t)(tok0 + (ok[it] ? tok : 0));
                 col[it] = nt * 256 + hh * 128 + q * 32 + c8[it];
                 if (ok[it]) {
-                  av[it] = *reinterpret_cast<const uint4*>(p.S + grow[it] * p.lds + col[it]);
-                  bv[it] = *reinterpret_cast<const uint4*>(p.S + grow[it] * p.lds + p.N + col[it]);
+                  if (EPI == WS_DSWIGLU8) {
+                    const uint8_t* qp = p.Q + grow[it] * p.lds + col[it];
+                    const float* sp = p.QS + grow[it] * (p.lds / 128) + col[it] / 128;
+                    aq[it] = *reinterpret_cast<const uint2*>(qp);
+                    bq[it] = *reinterpret_cast<const uint2*>(qp + p.N);
+                    as[it] = sp[0];
+                    bs[it] = sp[p.N / 128];
+                  } else {
+                    av[it] = *reinterpret_cast<const uint4*>(p.S + grow[it] * p.lds + col[it]);
+                    bv[it] = *reinterpret_cast<const uint4*>(p.S + grow[it] * p.lds + p.N + col[it]);
+                  }
                 }
               }
 #pragma unroll
@@ -392,14 +441,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const float4 d1 = *reinterpret_cast<const float4*>(pf + row[it] * 32 + c8[it] + 4);
                   const float dv[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
                   float fa[8], fb[8], oa[8], ob[8];
-                  Vec<__nv_bfloat16>::load(av[it], fa);
-                  Vec<__nv_bfloat16>::load(bv[it], fb);
+                  float hv[8];
+                  if (EPI == WS_DSWIGLU8) {
+                    e4m3x8(aq[it], as[it], fa);
+                    e4m3x8(bq[it], bs[it], fb);
+                  } else {
+                    Vec<__nv_bfloat16>::load(av[it], fa);
+                    Vec<__nv_bfloat16>::load(bv[it], fb);
+                  }
 #pragma unroll
                   for (int i = 0; i < 8; ++i) {
                     const float sg = __fdividef(1.0f, 1.0f + __expf(-fa[i]));
                     oa[i] = dv[i] * fb[i] * (sg * (1.0f + fa[i] * (1.0f - sg)));
                     ob[i] = dv[i] * fa[i] * sg;
+                    if (EPI == WS_DSWIGLU8) hv[i] = fa[i] * sg * fb[i];
                   }
+                  if (EPI == WS_DSWIGLU8)
+                    *reinterpret_cast<uint4*>(p.H + grow[it] * p.N + col[it]) =
+                        Vec<__nv_bfloat16>::store(hv);
                   *reinterpret_cast<uint4*>(p.C + grow[it] * p.ldc + col[it]) =
                       Vec<__nv_bfloat16>::store(oa);
                   *reinterpret_cast<uint4*>(p.C + grow[it] * p.ldc + p.N + col[it]) =
@@ -448,7 +507,66 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
+        if (EPI == WS_SWIGLU_SAVE8) {
+          // lane j of this warp: the largest |gate| and |up| of token c*32 + j
+          // over this warp's 32 columns, then over the tile's 128
+          float mg = 0.f, mu = 0.f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const uint32_t a = __reduce_max_sync(0xffffffffu, r0[j] & 0x7fffffffu);
+            const uint32_t b = __reduce_max_sync(0xffffffffu, r1[j] & 0x7fffffffu);
+            if (lane == j) { mg = __uint_as_float(a); mu = __uint_as_float(b); }
+          }
+          const int sl = ch * 2 + (int)(xit & 1u);
+          float* slot = amax_x + sl * 4 * 64;
+          slot[q * 64 + lane] = mg;
+          slot[q * 64 + 32 + lane] = mu;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&xbar[sl]);
+          xok = __all_sync(0xffffffffu, mbar_wait_bounded(&xbar[sl], (xit >> 1) & 1u, abort_flag,
+                                                          kWaitNs));
+          if (!xok) {
+            raise_abort(abort_flag, p.err);
+            break;
+          }
+          ++xit;
+#pragma unroll
+          for (int o = 0; o < 4; ++o) {
+            mg = fmaxf(mg, slot[o * 64 + lane]);
+            mu = fmaxf(mu, slot[o * 64 + 32 + lane]);
+          }
+          const float sg = amax_scale(mg), su = amax_scale(mu);
+          uint8_t* pb = reinterpret_cast<uint8_t*>(patch);       // [32 tok][32 col]
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float sc = __shfl_sync(0xffffffffu, hh ? su : sg, j);
+              pb[j * 32 + lane] = static_cast<uint8_t>(__nv_cvt_float_to_fp8(
+                  __fdiv_rn(__uint_as_float(hh ? r1[j] : r0[j]), sc), __NV_SATFINITE, __NV_E4M3));
+            }
+            __syncwarp();
+            const int colq = (hh ? p.N : 0) + nt * 128 + q * 32;
+#pragma unroll
+            for (int it = 0; it < 2; ++it) {
+              const int j = it * 16 + (lane >> 1);
+              const int tok = c * 32 + j;
+              const uint4 v = *reinterpret_cast<const uint4*>(pb + j * 32 + (lane & 1) * 16);
+              if (tok < count && in_bounds(tok0 + tok < p.rows, p.err))
+                *reinterpret_cast<uint4*>(p.Q + (size_t)(tok0 + tok) * p.lds + colq +
+                                          (lane & 1) * 16) = v;
+            }
+            __syncwarp();
+          }
+          const int tok = c * 32 + lane;
+          if (q == 0 && tok < count && in_bounds(tok0 + tok < p.rows, p.err)) {
+            float* sp = p.QS + (size_t)(tok0 + tok) * (p.lds / 128) + nt;
+            sp[0] = sg;
+            sp[p.N / 128] = su;
+          }
+        }
       }
+      if (!xok) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(tempty);
@@ -475,7 +593,8 @@ namespace {
 template <int EPI, bool WMN>
 moe_status ws_launch(const void* X, const void* W, int b_rows_per_group, const int32_t* offsets,
                      int n_groups, int rows, int N, int K, void* C, int ldc, void* S, int lds,
-                     const WsExtraGroups& ex, cudaStream_t s) {
+                     const WsExtraGroups& ex, cudaStream_t s, uint8_t* Q = nullptr,
+                     float* QS = nullptr, void* H = nullptr) {
   constexpr int OUT_COLS = TileMath<EPI>::OUT_COLS;
   CUtensorMap tmW, tmX, tmX128, tmX256, tmW2, tmX2, tmX2_128, tmX2_256;
   const int G = offsets ? n_groups : 1;
@@ -527,6 +646,9 @@ moe_status ws_launch(const void* X, const void* W, int b_rows_per_group, const i
   p.ldc = ldc;
   p.S = static_cast<__nv_bfloat16*>(S);
   p.lds = lds;
+  p.Q = Q;
+  p.QS = QS;
+  p.H = static_cast<__nv_bfloat16*>(H);
   p.n_extra = ex.n_extra;
   p.T_extra = ex.T;
   p.x_extra_local = ex.x_local ? 1 : 0;
@@ -587,6 +709,21 @@ moe_status launch_ws_gemm_ex(const void* X, const void* W, int b_rows_per_group,
                                          C, ldc, S, lds, ex, s);
   }
   return fail(MOE_ERR_INVALID_ARG, "ws gemm: unknown epilogue %d", (int)epi);
+}
+
+moe_status launch_ws_gate_up_save8(const void* X, const void* W, const int32_t* offsets,
+                                   int n_groups, int rows, int I, int d, void* h, uint8_t* a_q,
+                                   float* a_scale, cudaStream_t s) {
+  return ws_launch<WS_SWIGLU_SAVE8, false>(X, W, 2 * I, offsets, n_groups, rows, I, d, h, I,
+                                           nullptr, 2 * I, WsExtraGroups{}, s, a_q, a_scale);
+}
+
+moe_status launch_ws_dswiglu8(const void* dy, const void* W_down, const int32_t* offsets,
+                              int n_groups, int rows, int I, int d, const uint8_t* a_q,
+                              const float* a_scale, void* dA, void* h, cudaStream_t s) {
+  return ws_launch<WS_DSWIGLU8, true>(dy, W_down, 0, offsets, n_groups, rows, I, d, dA, 2 * I,
+                                      nullptr, 2 * I, WsExtraGroups{}, s,
+                                      const_cast<uint8_t*>(a_q), const_cast<float*>(a_scale), h);
 }
 
 }  // namespace moe

@@ -123,11 +123,22 @@ moe_status launch_ws2_gemm(const void* X, const void* W, int b_rows_per_group,
 //            DSWIGLU dh = the product (N = I columns), a = S[:, 0:I], b = S[:, I:2I]:
 //                    C[:, 0:I] = dh * b * SiLU'(a), C[:, I:2I] = dh * SiLU(a).
 // w_mn: W is stored [G*K rows][N cols] (N contiguous) instead of [G*rows_per_group][K].
-enum WsEpi { WS_SWIGLU = 0, WS_STORE = 1, WS_SWIGLU_SAVE = 2, WS_DSWIGLU = 3 };
+enum WsEpi { WS_SWIGLU = 0, WS_STORE = 1, WS_SWIGLU_SAVE = 2, WS_DSWIGLU = 3,
+             WS_SWIGLU_SAVE8 = 4, WS_DSWIGLU8 = 5 };   // the 8s: by their own launchers below
 moe_status launch_ws_gemm_ex(const void* X, const void* W, int b_rows_per_group,
                              const int32_t* offsets, int n_groups, int rows, int N, int K,
                              WsEpi epi, bool w_mn, void* C, int ldc, void* S, int lds,
                              cudaStream_t s, const WsExtraGroups* extra = nullptr);
+
+// SWIGLU_SAVE8  h [rows, I] bf16, and the float32 gate and up pre-activations as E4M3 a_q
+//               [rows, 2I] with a_scale [rows, 2I/128] (amax/448 per row and 128 columns)
+// DSWIGLU8      dA [rows, 2I] and h [rows, I] (bf16) from dy W_down and such a checkpoint
+moe_status launch_ws_gate_up_save8(const void* X, const void* W, const int32_t* offsets,
+                                   int n_groups, int rows, int I, int d, void* h, uint8_t* a_q,
+                                   float* a_scale, cudaStream_t s);
+moe_status launch_ws_dswiglu8(const void* dy, const void* W_down, const int32_t* offsets,
+                              int n_groups, int rows, int I, int d, const uint8_t* a_q,
+                              const float* a_scale, void* dA, void* h, cudaStream_t s);
 
 // gather.cu ------------------------------------------------------------------
 // Row-gather pipeline (bulk copies into a shared-memory ring, four producer
@@ -216,6 +227,30 @@ moe_status launch_unpermute_backward(const void* dh, const void* dx_shared, int 
 moe_status launch_router_weight_grad(const void* x, const int32_t* x_rows,
                                      const float* d_logit_perm, const int32_t* offsets,
                                      moe_dtype dt, int N_r, int d, float* dE, cudaStream_t s);
+
+// router_scored.cu -------------------------------------------------------------
+// Scores, biased and group-limited top-K, gates and load of moe_route_scored.
+size_t route_scored_ws_bytes(int T, int d, int N_r);
+moe_status launch_route_scored(const void* u, const void* E, moe_dtype dt, const float* b, int T,
+                               int d, int N_r, int K, int score, int n_groups, int topk_groups,
+                               int group_top, int renorm, float gate_scale, int32_t* idx,
+                               float* gate, int32_t* counts, float* logits, void* ws,
+                               cudaStream_t s);
+
+// router_loss.cu ---------------------------------------------------------------
+// Balance loss, and the scored router's gradients (off: sequence offsets or nullptr).
+size_t balance_ws_bytes(int T, int N_r, int n_seq);
+moe_status launch_balance_loss(const float* logits, const int32_t* idx, const int32_t* off,
+                               int n_seq, int T, int N_r, int K, int score, float alpha,
+                               float* loss, float* coef, void* ws, cudaStream_t s);
+size_t route_scored_bwd_ws_bytes(moe_dtype dt, int T, int d, int N_r);
+moe_status launch_route_scored_backward(const void* u, const void* E, moe_dtype dt,
+                                        const float* logits, const int32_t* idx,
+                                        const float* d_gate, const int32_t* off, int n_seq,
+                                        const float* coef, const float* d_loss, int T, int d,
+                                        int N_r, int K, int score, int renorm, float scale,
+                                        const void* du_base, float* d_logit, void* du, float* dE,
+                                        void* ws, cudaStream_t s);
 
 // ep.cu ----------------------------------------------------------------------
 // Expert-parallel receive layout, dispatch and return (see ep.cu's header).
