@@ -2,15 +2,368 @@
 // and group-limited top-K, gates, load.
 //
 // Logits come as S partial sums over slices of d, [S][T][ld]:
-//   float64 (router_logits64_kernel): float32 inputs, and few bf16 tokens;
-//     every key is then the definition's and nothing has to be redone.
-// A warp per token joins the slices and routes (router_select.cuh).
+//   float32 inputs: float64 on CUDA cores (router_logits64_kernel);
+//   few bf16 tokens: float64, a block per expert (router_logits_few_kernel);
+//   else bf16 on tcgen05 CTA pairs, float32 (router_logits_tc_kernel).
+// A warp per token joins the slices and routes (router_select.cuh).  From
+// float64 logits the keys are the definition's; from float32 ones the tokens
+// with a close decision are listed and routed again from float64 logits of
+// the experts that can take part in it (router_recheck_kernel).
+//
+// Every wait is bounded (1 s of %globaltimer) and reported through the device
+// error word.
 #include "launch.h"
 #include "router_select.cuh"
+#include "sm100.cuh"
 
 namespace moe {
 
+moe_status make_tmap_2d(CUtensorMap* tm, const void* base, CUtensorMapDataType dtype,
+                        int elem_bytes, uint64_t inner, uint64_t outer, uint32_t box_inner,
+                        uint32_t box_outer);
+
 namespace {
+
+using namespace sm100;
+
+// ---------------------------------------------------------------- tensor-core logits
+// A CTA pair (cta_group::2) owns 256 tokens x Nt <= 256 experts x one slice of
+// d: each CTA stages its 128 token rows (the MMA's M side) and half of the
+// experts, so the pair streams each centroid byte once.  The token side is
+// read once from memory; what bounds the kernel is the shared-memory fill
+// (u and E tiles through L2), then the copy of u itself.
+//
+// The tensor core adds into its accumulator with truncation: over the whole
+// of d = 7168 that biases a logit by some 3e-6 of its size.  The sum is
+// therefore cut every kChunk blocks of 64 (32 accumulation steps): two TMEM
+// buffers take turns, and the epilogue warps add each finished chunk into
+// float32 registers (round to nearest) while the next one runs.
+constexpr int BK = 64;                 // bf16 K elements per 128-byte swizzle row
+constexpr int TM = 128;                // token rows per CTA (TMEM lanes)
+constexpr int kMaxN = 256;
+constexpr int kChunk = 8;
+constexpr int STAGES = 6;
+constexpr int kEpiWarps = 16;          // four per TMEM lane quarter, 16-column pieces in turn
+constexpr int kTcThreads = 64 + 32 * kEpiWarps;
+constexpr int kPieces = kMaxN / 16 / (kEpiWarps / 4);
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr int A_BYTES = TM * BK * 2;
+constexpr int B_BYTES = (kMaxN / 2) * BK * 2;
+constexpr int OFF_B = STAGES * A_BYTES;
+constexpr int OFF_BAR = OFF_B + STAGES * B_BYTES;
+constexpr int N_BARS = 2 * STAGES + 5;           // full, empty, tfull[2], tempty[2], mma_done
+constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
+constexpr int SMEM_BYTES = OFF_MISC + 16;
+constexpr int SMEM_ALLOC = SMEM_BYTES + 1024;
+
+struct LogitParams {
+  int T, N_r, nk, S;
+  int n_tt, n_et, Nt;       // token tiles of 256, expert tiles of Nt
+  int ld;                   // n_et * Nt
+  float* P;                 // [S][T][ld]
+  int32_t* counts;          // zeroed here, as is the listing's length
+  int32_t* n_listed;
+  int* err;
+};
+
+__device__ __forceinline__ void raise_abort(volatile int* abort, int* err) {
+  *abort = 1;
+  atomicOr(err, ERR_GEMM_TIMEOUT);
+}
+
+__global__ void __launch_bounds__(kTcThreads, 1)
+    router_logits_tc_kernel(const __grid_constant__ CUtensorMap tmU,
+                            const __grid_constant__ CUtensorMap tmE, const LogitParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + OFF_B;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* mma_done = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t half = cluster_ctarank();           // which 128 tokens, which half of the experts
+  const bool is_leader = half == 0;
+  const int Nt = p.Nt;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * kEpiWarps);          // the epilogue warps of both CTAs
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmU);
+    tma_prefetch_desc(&tmE);
+  }
+  if (warp == 1) {
+    tmem2_alloc(tmem_slot, 512);
+    tmem2_relinquish();
+  }
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < p.N_r; i += blockDim.x) p.counts[i] = 0;
+    if (threadIdx.x == 0) *p.n_listed = 0;
+  }
+  tc_fence_before();
+  cluster_sync_all();          // barriers initialised in both CTAs, TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t full_leader0 = map_shared_to(smem_u32(&full[0]), 0);
+  const uint32_t tempty_leader0 = map_shared_to(smem_u32(&tempty[0]), 0);
+  const int items = p.n_tt * p.n_et * p.S, step = (int)n_clusters_x();
+  const int first = (int)cluster_id_x();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      const uint32_t bytes = 2u * (uint32_t)(A_BYTES + (Nt / 2) * BK * 2);
+      for (int it = first; it < items && ok; it += step) {
+        const int et = it % p.n_et, sl = (it / p.n_et) % p.S, tt = it / p.n_et / p.S;
+        const int row0 = tt * 2 * TM + (int)half * TM, e0 = et * Nt + (int)half * (Nt / 2);
+        const int kb1 = (sl + 1) * p.nk / p.S;
+        for (int kb = sl * p.nk / p.S; kb < kb1; ++kb) {
+          if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitNs)) {
+            raise_abort(abort_flag, p.err);
+            ok = false;
+            break;
+          }
+          if (is_leader) mbar_arrive_expect_tx(&full[stage], bytes);
+          const uint32_t fb = full_leader0 + stage * 8;
+          tma_load_2d_pair(sA + stage * A_BYTES, &tmU, kb * BK, row0, fb);
+          tma_load_2d_pair(sB + stage * B_BYTES, &tmE, kb * BK, e0, fb);
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+      }
+      // the leader waits until every armed stage's copies have landed
+      if (is_leader)
+        for (int s = 0; s < STAGES; ++s)
+          mbar_wait_bounded(&full[s], ((s < stage) ? phase : phase ^ 1), nullptr, kWaitNs);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (pair leader)
+    if (is_leader && lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(2 * TM, Nt);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, tphase = 0;
+      bool ok = true;
+      for (int it = first; it < items && ok; it += step) {
+        const int sl = (it / p.n_et) % p.S;
+        const int kb0 = sl * p.nk / p.S, kb1 = (sl + 1) * p.nk / p.S;
+        for (int c0 = kb0; c0 < kb1 && ok; c0 += kChunk) {
+          if (!mbar_wait_bounded(&tempty[buf], tphase ^ 1, abort_flag, kWaitNs)) {
+            raise_abort(abort_flag, p.err);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int c1 = min(kb1, c0 + kChunk);
+          for (int kb = c0; kb < c1; ++kb) {
+            if (!mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitNs)) {
+              raise_abort(abort_flag, p.err);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a0 = smem_u32(sA + stage * A_BYTES);
+            const uint32_t b0 = smem_u32(sB + stage * B_BYTES);
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k)
+              mma2_f16_ss(tmem_base + buf * kMaxN, smem_desc_k_sw128(a0 + k * 32),
+                          smem_desc_k_sw128(b0 + k * 32), idesc, (kb > c0 || k > 0) ? 1u : 0u);
+            mma2_commit_mask(&empty[stage], 3);
+            if (++stage == STAGES) { stage = 0; phase ^= 1; }
+          }
+          if (!ok) break;
+          mma2_commit_mask(&tfull[buf], 3);
+          if (++buf == 2) { buf = 0; tphase ^= 1; }
+        }
+      }
+      mma2_commit_local(mma_done);
+      mbar_wait_bounded(mma_done, 0, nullptr, kWaitNs);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3, part = (warp - 2) >> 2;
+    const int n_pieces = Nt / 16;
+    const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    int buf = 0;
+    uint32_t tphase = 0;
+    bool ok = true;
+    for (int it = first; it < items && ok; it += step) {
+      const int et = it % p.n_et, sl = (it / p.n_et) % p.S, tt = it / p.n_et / p.S;
+      const int kb0 = sl * p.nk / p.S, kb1 = (sl + 1) * p.nk / p.S;
+      float acc[kPieces][16];
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[i][j] = 0.f;
+      for (int c0 = kb0; c0 < kb1; c0 += kChunk) {
+        const bool got = mbar_wait_bounded(&tfull[buf], tphase, abort_flag, kWaitNs);
+        if (!__all_sync(0xffffffffu, got)) {
+          if (lane == 0) raise_abort(abort_flag, p.err);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int piece = part + i * (kEpiWarps / 4);
+          if (piece < n_pieces) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(trow + buf * kMaxN + piece * 16, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[i][j] += __uint_as_float(r[j]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty_leader0 + buf * 8);
+        if (++buf == 2) { buf = 0; tphase ^= 1; }
+      }
+      if (!ok) break;
+      const int t = tt * 2 * TM + (int)half * TM + q * 32 + lane;
+      if (t < p.T) {
+        float* out = p.P + ((size_t)sl * p.T + t) * p.ld + et * Nt;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int piece = part + i * (kEpiWarps / 4);
+          if (piece < n_pieces) {
+            float4* o = reinterpret_cast<float4*>(out + piece * 16);
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              o[v] = make_float4(acc[i][4 * v], acc[i][4 * v + 1], acc[i][4 * v + 2],
+                                 acc[i][4 * v + 3]);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();          // no CTA leaves while the other may still use its barriers or TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    tmem2_dealloc(tmem_base, 512);
+  }
+}
+
+// CTA pairs of the logits kernel that run at once.
+int resident_pairs() {
+  static int cached[kMaxSmemDevices] = {};
+  static bool attr_done[kMaxSmemDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxSmemDevices) return 0;
+  const void* kern = reinterpret_cast<const void*>(router_logits_tc_kernel);
+  if (ensure_max_smem(kern, SMEM_ALLOC, attr_done, "router_logits smem attribute") != MOE_OK)
+    return 0;
+  if (cached[dev]) return cached[dev];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (sm_count() / 2));
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = SMEM_ALLOC;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    return 0;
+  }
+  cached[dev] = n;
+  return n;
+}
+
+// Tiling of the tensor-core logits: expert tiles of equal width, as many
+// slices of d as fill the GPU once (fewer tokens: more slices; a slice keeps
+// at least four blocks of 64).  148 SMs are 74 pairs; the workspace is sized
+// for that many.
+constexpr int kPairs = 74, kMaxSlices = 16;
+struct LogitTiling {
+  int n_tt, n_et, Nt, S, ld;
+};
+LogitTiling logit_tiling(int T, int d, int N) {
+  LogitTiling L;
+  L.n_tt = (T + 2 * TM - 1) / (2 * TM);
+  L.n_et = (N + kMaxN - 1) / kMaxN;
+  L.Nt = ((N + L.n_et - 1) / L.n_et + 31) / 32 * 32;
+  L.ld = L.n_et * L.Nt;
+  int S = kPairs / (L.n_tt * L.n_et);
+  if (S > d / BK / 4) S = d / BK / 4;
+  if (S > kMaxSlices) S = kMaxSlices;
+  L.S = S < 1 ? 1 : S;
+  return L;
+}
+
+// ---------------------------------------------------------------- few tokens
+// A block per expert, TT tokens at once: float64 sums of the products, which
+// are exact in float32 (two 8-bit significands) unless they fall below 2^-126.
+// Latency-bound: all of a thread's row pieces are in flight together.
+template <int TT>
+__global__ void __launch_bounds__(128) router_logits_few_kernel(
+    const __nv_bfloat16* __restrict__ u, const __nv_bfloat16* __restrict__ E, int T, int d, int N,
+    double* __restrict__ P, int32_t* __restrict__ counts) {
+  __shared__ double part[4][TT];
+  const int e = blockIdx.x, tid = threadIdx.x, nv = d / 8;
+  if (e == 0)
+    for (int i = tid; i < N; i += 128) counts[i] = 0;
+  const uint4* er = reinterpret_cast<const uint4*>(E + (size_t)e * d);
+  double a[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) a[t] = 0.0;
+  constexpr int U = 8;
+  for (int v0 = tid; v0 < nv; v0 += 128 * U) {
+    uint4 w[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const int v = v0 + 128 * q;
+      w[q] = v < nv ? __ldg(er + v) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      if (t >= T) break;
+      const uint4* ur = reinterpret_cast<const uint4*>(u + (size_t)t * d);
+      uint4 x[U];
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        const int v = v0 + 128 * q;
+        x[q] = v < nv ? __ldg(ur + v) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        float fx[8], fw[8];
+        Vec<__nv_bfloat16>::load(x[q], fx);
+        Vec<__nv_bfloat16>::load(w[q], fw);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[t] += (double)(fx[i] * fw[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    a[t] = sel_warp_sum(a[t]);
+    if ((tid & 31) == 0) part[tid >> 5][t] = a[t];
+  }
+  __syncthreads();
+  if (tid < TT && tid < T)
+    P[(size_t)tid * N + e] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+}
+constexpr int kFewTokens = 8;
 
 // ---------------------------------------------------------------- float64 logits
 // P[s][t][i] = sum over slice s of d of u[t,k] E[i,k], float64 products and
@@ -96,6 +449,157 @@ __global__ void __launch_bounds__(256) router_select64_kernel(
     if (hist[i]) atomicAdd(&counts[i], hist[i]);
 }
 
+// The tokens listed for the exact pass: how many, their ids, per token 32
+// words of expert masks (word l, bit j: expert j*32 + l), the finished shares
+// of its float64 logits, and those logits.
+struct Recheck {
+  int32_t* n;
+  int32_t* tok;
+  uint32_t* mask;
+  int32_t* done;
+  double* x;
+};
+
+template <int V>
+__global__ void __launch_bounds__(256) router_select_kernel(
+    const float* __restrict__ P, int S, int ld, const float* __restrict__ bias, int T,
+    SelectRule r, int32_t* __restrict__ idx, float* __restrict__ gate,
+    int32_t* __restrict__ counts, float* __restrict__ logits, Recheck rc) {
+  extern __shared__ int hist[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wpb = blockDim.x >> 5;
+  const int N = r.N_r;
+  float* wk = reinterpret_cast<float*>(hist + N) + (size_t)warp * N;
+  for (int i = threadIdx.x; i < N; i += blockDim.x) hist[i] = 0;
+  __syncthreads();
+  for (int t = blockIdx.x * wpb + warp; t < T; t += gridDim.x * wpb) {
+    const float* row = P + (size_t)t * ld;
+    const size_t stride = (size_t)T * ld;
+    // the slices' sums, joined in float64 and rounded once
+    float x[V], mag = 0.f;
+    {
+      double a[V];
+      float m[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) { a[j] = 0.0; m[j] = 0.f; }
+      for (int s = 0; s < S; ++s) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int e = j * 32 + lane;
+          const float v = e < N ? row[s * stride + e] : 0.f;
+          a[j] += (double)v;
+          m[j] += fabsf(v);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int e = j * 32 + lane;
+        x[j] = (float)a[j];
+        mag = fmaxf(mag, m[j]);
+        if (logits && e < N) logits[(size_t)t * N + e] = x[j];
+      }
+    }
+    mag = sel_warp_max(mag);
+    const auto getx = [&](int e) {
+      double a = 0.0;
+      for (int s = 0; s < S; ++s) a += (double)row[s * stride + e];
+      return (float)a;
+    };
+    const CloseCall cc = select_token<V, float>(x, getx, bias, r, mag, wk,
+                                                idx + (size_t)t * r.K, gate + (size_t)t * r.K);
+    for (int k = lane; k < r.K; k += 32) atomicAdd(&hist[idx[(size_t)t * r.K + k]], 1);
+    if (__any_sync(0xffffffffu, cc.close)) {
+      int slot = 0;
+      if (lane == 0) {
+        slot = atomicAdd(rc.n, 1);
+        rc.tok[slot] = t;
+        rc.done[slot] = 0;
+      }
+      slot = __shfl_sync(0xffffffffu, slot, 0);
+      rc.mask[(size_t)slot * 32 + lane] = cc.mask;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < N; i += blockDim.x)
+    if (hist[i]) atomicAdd(&counts[i], hist[i]);
+}
+
+// The listed tokens again.  A share is eight experts of one token, a warp per
+// expert (float64 sum of the exact products); the block that finishes a
+// token's last share routes it, with exact logits where the mask asks for
+// them and the float32 ones elsewhere (too far off to matter).
+constexpr int kShare = 8;
+template <int V>
+__global__ void __launch_bounds__(32 * kShare) router_recheck_kernel(
+    const __nv_bfloat16* __restrict__ u, const __nv_bfloat16* __restrict__ E,
+    const float* __restrict__ P, int S, int ld, const float* __restrict__ bias, int T, int d,
+    SelectRule r, int32_t* __restrict__ idx, float* __restrict__ gate,
+    int32_t* __restrict__ counts, Recheck rc) {
+  extern __shared__ float wk[];
+  __shared__ int last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, N = r.N_r;
+  const int shares = (N + kShare - 1) / kShare, nv = d / 8;
+  const int n = *rc.n;
+  for (long long w = blockIdx.x; w < (long long)n * shares; w += gridDim.x) {
+    const int i = (int)(w / shares), sh = (int)(w - (long long)i * shares);
+    const int t = rc.tok[i], e = sh * kShare + warp;
+    const uint32_t* mask = rc.mask + (size_t)i * 32;
+    if (e < N && ((mask[e & 31] >> (e >> 5)) & 1u)) {
+      const uint4* ur = reinterpret_cast<const uint4*>(u + (size_t)t * d);
+      const uint4* er = reinterpret_cast<const uint4*>(E + (size_t)e * d);
+      double a = 0.0, b = 0.0;
+      constexpr int U = 4;
+      for (int v0 = lane; v0 < nv; v0 += 32 * U) {
+        uint4 x[U], y[U];
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          const int v = v0 + 32 * q;
+          x[q] = v < nv ? ur[v] : make_uint4(0, 0, 0, 0);
+          y[q] = v < nv ? er[v] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          float fx[8], fy[8];
+          Vec<__nv_bfloat16>::load(x[q], fx);
+          Vec<__nv_bfloat16>::load(y[q], fy);
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            a += (double)(fx[k] * fy[k]);
+            b += (double)(fx[k + 1] * fy[k + 1]);
+          }
+        }
+      }
+      a = sel_warp_sum(a + b);
+      if (lane == 0) rc.x[(size_t)i * N + e] = a;
+    }
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(&rc.done[i], 1) == shares - 1;
+    __syncthreads();
+    if (last && warp == 0) {
+      __threadfence();
+      const float* row = P + (size_t)t * ld;
+      const size_t stride = (size_t)T * ld;
+      const auto getx = [&](int q) {
+        if ((mask[q & 31] >> (q >> 5)) & 1u) return __ldcg(rc.x + (size_t)i * N + q);
+        double a = 0.0;
+        for (int s = 0; s < S; ++s) a += (double)row[s * stride + q];
+        return (double)(float)a;
+      };
+      double x[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int q = j * 32 + lane;
+        x[j] = q < N ? getx(q) : 0.0;
+      }
+      int32_t* ti = idx + (size_t)t * r.K;
+      for (int k = lane; k < r.K; k += 32) atomicSub(&counts[ti[k]], 1);
+      select_token<V, double>(x, getx, bias, r, 0.f, wk, ti, gate + (size_t)t * r.K);
+      for (int k = lane; k < r.K; k += 32) atomicAdd(&counts[ti[k]], 1);
+    }
+    __syncthreads();
+  }
+}
+
 // Slices of d for the float64 logits: enough blocks for two per SM, at most
 // kMaxSlices64, each slice at least 128 columns.
 constexpr int kMaxSlices64 = 16;
@@ -112,10 +616,73 @@ int dispatch_v(int N) {
   return V <= 1 ? 1 : V <= 2 ? 2 : V <= 4 ? 4 : V <= 8 ? 8 : V <= 16 ? 16 : 32;
 }
 
+// Workspace of the tensor-core path: partial logits, then the listing.
+size_t tc_ws_bytes(int T, int d, int N, Recheck* rc, uint8_t* base) {
+  const LogitTiling L = logit_tiling(T, d, N);
+  size_t o = 0;
+  auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes, 256); return at; };
+  take((size_t)L.S * T * L.ld * 4);
+  const size_t n = take(4), tok = take((size_t)T * 4), mask = take((size_t)T * 128),
+               done = take((size_t)T * 4), x = take((size_t)T * N * 8);
+  if (rc) {
+    rc->n = reinterpret_cast<int32_t*>(base + n);
+    rc->tok = reinterpret_cast<int32_t*>(base + tok);
+    rc->mask = reinterpret_cast<uint32_t*>(base + mask);
+    rc->done = reinterpret_cast<int32_t*>(base + done);
+    rc->x = reinterpret_cast<double*>(base + x);
+  }
+  return o;
+}
+
+moe_status launch_logits_tc(const void* u, const void* E, int T, int d, int N, float* P,
+                            int32_t* counts, int32_t* n_listed, cudaStream_t s) {
+  const LogitTiling L = logit_tiling(T, d, N);
+  CUtensorMap tmU, tmE;
+  moe_status st = make_tmap_2d(&tmU, u, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d, T, BK, TM);
+  if (st != MOE_OK) return st;
+  st = make_tmap_2d(&tmE, E, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d, N, BK, L.Nt / 2);
+  if (st != MOE_OK) return st;
+  LogitParams p;
+  p.T = T;
+  p.N_r = N;
+  p.nk = d / BK;
+  p.S = L.S;
+  p.n_tt = L.n_tt;
+  p.n_et = L.n_et;
+  p.Nt = L.Nt;
+  p.ld = L.ld;
+  p.P = P;
+  p.counts = counts;
+  p.n_listed = n_listed;
+  p.err = device_error_word();
+  if (!p.err) return fail(MOE_ERR_CUDA, "device error word unavailable");
+  const int pairs = resident_pairs();
+  if (pairs <= 0) return fail(MOE_ERR_CUDA, "router_logits: no resident CTA pair");
+  const long long items = (long long)L.n_tt * L.n_et * L.S;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (unsigned)(items < pairs ? items : pairs));
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = SMEM_ALLOC;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, router_logits_tc_kernel, tmU, tmE, p),
+                    "router_logits launch");
+}
+
 }  // namespace
 
 size_t route_scored_ws_bytes(int T, int d, int N_r) {
-  return align_up((size_t)slices64(T, d, N_r) * T * N_r * sizeof(double), 256);
+  // the larger of the float64 and the tensor-core path's needs: the dtype is
+  // not among the arguments
+  const size_t a = align_up((size_t)slices64(T, d, N_r) * T * N_r * sizeof(double), 256);
+  const size_t b = tc_ws_bytes(T, d, N_r, nullptr, nullptr);
+  return a > b ? a : b;
 }
 
 moe_status launch_route_scored(const void* u, const void* E, moe_dtype dt, const float* b, int T,
@@ -123,33 +690,66 @@ moe_status launch_route_scored(const void* u, const void* E, moe_dtype dt, const
                                int group_top, int renorm, float gate_scale, int32_t* idx,
                                float* gate, int32_t* counts, float* logits, void* ws,
                                cudaStream_t s) {
+  using bf = __nv_bfloat16;
   const SelectRule r{N_r, K, score, n_groups, topk_groups, group_top, renorm, gate_scale};
-  double* P = static_cast<double*>(ws);
-  const int S = slices64(T, d, N_r);
-  const dim3 grid((T + kT64 - 1) / kT64, (N_r + kT64 - 1) / kT64, S);
-  if (dt == MOE_F32)
-    router_logits64_kernel<float><<<grid, 256, 0, s>>>(static_cast<const float*>(u),
-                                                       static_cast<const float*>(E), T, d, N_r, S,
-                                                       N_r, P, counts);
-  else
-    router_logits64_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(
-        static_cast<const __nv_bfloat16*>(u), static_cast<const __nv_bfloat16*>(E), T, d, N_r, S,
-        N_r, P, counts);
-  moe_status st = cuda_check(cudaGetLastError(), "router_logits64 launch");
-  if (st != MOE_OK) return st;
-  const int wpb = 4;
+  moe_status st;
+  const int V = dispatch_v(N_r);
+  // warps per block of the selection: one while that fills no SM twice
+  const int wpb = T <= 2 * sm_count() ? 1 : 4;
   int blocks = (T + wpb - 1) / wpb;
   if (blocks > 16 * sm_count()) blocks = 16 * sm_count();
   const size_t smem = (size_t)N_r * sizeof(int) * (1 + wpb);
+  if (dt == MOE_BF16 && T > kFewTokens) {
+    float* P = static_cast<float*>(ws);
+    Recheck rc;
+    tc_ws_bytes(T, d, N_r, &rc, static_cast<uint8_t*>(ws));
+    const LogitTiling L = logit_tiling(T, d, N_r);
+    st = launch_logits_tc(u, E, T, d, N_r, P, counts, rc.n, s);
+    if (st != MOE_OK) return st;
+#define MOE_SELECT(v)                                                                        \
+  case v:                                                                                    \
+    router_select_kernel<v><<<blocks, wpb * 32, smem, s>>>(P, L.S, L.ld, b, T, r, idx, gate, \
+                                                           counts, logits, rc);              \
+    break;
+    switch (V) { MOE_SELECT(1) MOE_SELECT(2) MOE_SELECT(4) MOE_SELECT(8) MOE_SELECT(16) MOE_SELECT(32) }
+#undef MOE_SELECT
+    st = cuda_check(cudaGetLastError(), "router_select launch");
+    if (st != MOE_OK) return st;
+    const int rblocks = 4 * sm_count();
+#define MOE_RECHECK(v)                                                                       \
+  case v:                                                                                    \
+    router_recheck_kernel<v><<<rblocks, 32 * kShare, N_r * sizeof(float), s>>>(              \
+        static_cast<const bf*>(u), static_cast<const bf*>(E), P, L.S, L.ld, b, T, d, r, idx, \
+        gate, counts, rc);                                                                   \
+    break;
+    switch (V) { MOE_RECHECK(1) MOE_RECHECK(2) MOE_RECHECK(4) MOE_RECHECK(8) MOE_RECHECK(16) MOE_RECHECK(32) }
+#undef MOE_RECHECK
+    return cuda_check(cudaGetLastError(), "router_recheck launch");
+  }
+  double* P = static_cast<double*>(ws);
+  int S = 1;
+  if (dt == MOE_F32) {
+    S = slices64(T, d, N_r);
+    const dim3 grid((T + kT64 - 1) / kT64, (N_r + kT64 - 1) / kT64, S);
+    router_logits64_kernel<float><<<grid, 256, 0, s>>>(static_cast<const float*>(u),
+                                                       static_cast<const float*>(E), T, d, N_r, S,
+                                                       N_r, P, counts);
+  } else {
+    const bf* ub = static_cast<const bf*>(u);
+    const bf* eb = static_cast<const bf*>(E);
+    if (T <= 1) router_logits_few_kernel<1><<<N_r, 128, 0, s>>>(ub, eb, T, d, N_r, P, counts);
+    else if (T <= 2) router_logits_few_kernel<2><<<N_r, 128, 0, s>>>(ub, eb, T, d, N_r, P, counts);
+    else if (T <= 4) router_logits_few_kernel<4><<<N_r, 128, 0, s>>>(ub, eb, T, d, N_r, P, counts);
+    else router_logits_few_kernel<8><<<N_r, 128, 0, s>>>(ub, eb, T, d, N_r, P, counts);
+  }
+  st = cuda_check(cudaGetLastError(), "router float64 logits launch");
+  if (st != MOE_OK) return st;
 #define MOE_SELECT64(v)                                                                      \
   case v:                                                                                    \
     router_select64_kernel<v><<<blocks, wpb * 32, smem, s>>>(P, S, N_r, b, T, r, idx, gate,  \
                                                              counts, logits);                \
     break;
-  switch (dispatch_v(N_r)) {
-    MOE_SELECT64(1) MOE_SELECT64(2) MOE_SELECT64(4) MOE_SELECT64(8) MOE_SELECT64(16)
-    MOE_SELECT64(32)
-  }
+  switch (V) { MOE_SELECT64(1) MOE_SELECT64(2) MOE_SELECT64(4) MOE_SELECT64(8) MOE_SELECT64(16) MOE_SELECT64(32) }
 #undef MOE_SELECT64
   return cuda_check(cudaGetLastError(), "router_select64 launch");
 }
