@@ -416,52 +416,42 @@ __global__ void __launch_bounds__(256) router_logits64_kernel(
 // ---------------------------------------------------------------- selection
 // A warp per token; the block's load histogram in shared memory, then added to
 // counts (whole numbers: the order of the additions does not matter).
-template <int V>
-__global__ void __launch_bounds__(256) router_select64_kernel(
-    const double* __restrict__ P, int S, int ld, const float* __restrict__ bias, int T,
-    SelectRule r, int32_t* __restrict__ idx, float* __restrict__ gate,
-    int32_t* __restrict__ counts, float* __restrict__ logits) {
-  extern __shared__ int hist[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wpb = blockDim.x >> 5;
-  const int N = r.N_r;
-  float* wk = reinterpret_cast<float*>(hist + N) + (size_t)warp * N;
-  for (int i = threadIdx.x; i < N; i += blockDim.x) hist[i] = 0;
-  __syncthreads();
-  for (int t = blockIdx.x * wpb + warp; t < T; t += gridDim.x * wpb) {
-    const auto getx = [&](int e) {
-      double v = 0.0;
-      for (int s = 0; s < S; ++s) v += P[((size_t)s * T + t) * ld + e];
-      return v;
-    };
-    double x[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int e = j * 32 + lane;
-      x[j] = e < N ? getx(e) : 0.0;
-      if (logits && e < N) logits[(size_t)t * N + e] = (float)x[j];
-    }
-    select_token<V, double>(x, getx, bias, r, 0.f, wk, idx + (size_t)t * r.K,
-                            gate + (size_t)t * r.K);
-    for (int k = lane; k < r.K; k += 32) atomicAdd(&hist[idx[(size_t)t * r.K + k]], 1);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < N; i += blockDim.x)
-    if (hist[i]) atomicAdd(&counts[i], hist[i]);
-}
 
-// The tokens listed for the exact pass: how many, their ids, per token 32
-// words of expert masks (word l, bit j: expert j*32 + l), the finished shares
-// of its float64 logits, and those logits.
+// The tokens listed for the exact pass: how many, and their ids.
 struct Recheck {
   int32_t* n;
   int32_t* tok;
-  uint32_t* mask;
-  int32_t* done;
-  double* x;
 };
 
+// x[j]: the slices' sums, joined in float64 and rounded once; returns the
+// largest sum over slices of |partial| among this lane's experts.
 template <int V>
-__global__ void __launch_bounds__(256) router_select_kernel(
+__device__ __forceinline__ float join_slices(const float* __restrict__ row, int S, size_t stride,
+                                             int N, float (&x)[V]) {
+  const int lane = threadIdx.x & 31;
+  double a[V];
+  float m[V], mag = 0.f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) { a[j] = 0.0; m[j] = 0.f; }
+  for (int s = 0; s < S; ++s) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int e = j * 32 + lane;
+      const float v = e < N ? row[s * stride + e] : 0.f;
+      a[j] += (double)v;
+      m[j] += fabsf(v);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    x[j] = (float)a[j];
+    mag = fmaxf(mag, m[j]);
+  }
+  return mag;
+}
+
+template <int V>
+__global__ void __launch_bounds__(128) router_select_kernel(
     const float* __restrict__ P, int S, int ld, const float* __restrict__ bias, int T,
     SelectRule r, int32_t* __restrict__ idx, float* __restrict__ gate,
     int32_t* __restrict__ counts, float* __restrict__ logits, Recheck rc) {
@@ -472,130 +462,118 @@ __global__ void __launch_bounds__(256) router_select_kernel(
   for (int i = threadIdx.x; i < N; i += blockDim.x) hist[i] = 0;
   __syncthreads();
   for (int t = blockIdx.x * wpb + warp; t < T; t += gridDim.x * wpb) {
-    const float* row = P + (size_t)t * ld;
-    const size_t stride = (size_t)T * ld;
-    // the slices' sums, joined in float64 and rounded once
-    float x[V], mag = 0.f;
-    {
-      double a[V];
-      float m[V];
+    float x[V], sc[V], key[V];
+    const float mag = sel_warp_max(join_slices<V>(P + (size_t)t * ld, S, (size_t)T * ld, N, x));
+    if (logits) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) { a[j] = 0.0; m[j] = 0.f; }
-      for (int s = 0; s < S; ++s) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const int e = j * 32 + lane;
-          const float v = e < N ? row[s * stride + e] : 0.f;
-          a[j] += (double)v;
-          m[j] += fabsf(v);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int e = j * 32 + lane;
-        x[j] = (float)a[j];
-        mag = fmaxf(mag, m[j]);
-        if (logits && e < N) logits[(size_t)t * N + e] = x[j];
-      }
+      for (int j = 0; j < V; ++j)
+        if (j * 32 + lane < N) logits[(size_t)t * N + j * 32 + lane] = x[j];
     }
-    mag = sel_warp_max(mag);
-    const auto getx = [&](int e) {
-      double a = 0.0;
-      for (int s = 0; s < S; ++s) a += (double)row[s * stride + e];
-      return (float)a;
-    };
-    const CloseCall cc = select_token<V, float>(x, getx, bias, r, mag, wk,
-                                                idx + (size_t)t * r.K, gate + (size_t)t * r.K);
-    for (int k = lane; k < r.K; k += 32) atomicAdd(&hist[idx[(size_t)t * r.K + k]], 1);
-    if (__any_sync(0xffffffffu, cc.close)) {
-      int slot = 0;
-      if (lane == 0) {
-        slot = atomicAdd(rc.n, 1);
-        rc.tok[slot] = t;
-        rc.done[slot] = 0;
-      }
-      slot = __shfl_sync(0xffffffffu, slot, 0);
-      rc.mask[(size_t)slot * 32 + lane] = cc.mask;
+    const float logit_err = mag == 0.f ? 0.f : kLogitError * fmaxf(4.f, mag);
+    int32_t* ti = idx + (size_t)t * r.K;
+    const TokenScale ts = select_keys<V>(x, bias, r, logit_err, sc, key);
+    const Selection sel = select_core<V>(key, ts.err, r, wk, ti);
+    if (sel.open) {
+      if (lane == 0) rc.tok[atomicAdd(rc.n, 1)] = t;
+      continue;                                     // its gates and load come with the exact pass
     }
+    select_gates<V, float>(x, sel.e, ts.m, ts.z, r, ti, gate + (size_t)t * r.K);
+    for (int k = lane; k < r.K; k += 32) atomicAdd(&hist[r.K <= 32 ? sel.e : ti[k]], 1);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < N; i += blockDim.x)
     if (hist[i]) atomicAdd(&counts[i], hist[i]);
 }
 
-// The listed tokens again.  A share is eight experts of one token, a warp per
-// expert (float64 sum of the exact products); the block that finishes a
-// token's last share routes it, with exact logits where the mask asks for
-// them and the float32 ones elsewhere (too far off to matter).
-constexpr int kShare = 8;
-template <int V>
-__global__ void __launch_bounds__(32 * kShare) router_recheck_kernel(
+// A block per token, a thread per expert (router_select.cuh): every token, or
+// the listed ones (rc.tok, the first pass left their decisions open).
+//   EXACT   P holds float64 slices
+//   else    float32 slices; the experts that open decisions wait for get
+//           float64 logits, eight at a time, their products spread over the
+//           block (exact in float32 unless below 2^-126).  Usually two or
+//           three experts and one turn.
+constexpr int kDots = 8;
+template <bool EXACT, int MAXT>
+__global__ void __launch_bounds__(MAXT) router_token_kernel(
     const __nv_bfloat16* __restrict__ u, const __nv_bfloat16* __restrict__ E,
-    const float* __restrict__ P, int S, int ld, const float* __restrict__ bias, int T, int d,
+    const void* __restrict__ P, int S, int ld, const float* __restrict__ bias, int T, int d,
     SelectRule r, int32_t* __restrict__ idx, float* __restrict__ gate,
-    int32_t* __restrict__ counts, Recheck rc) {
-  extern __shared__ float wk[];
-  __shared__ int last;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, N = r.N_r;
-  const int shares = (N + kShare - 1) / kShare, nv = d / 8;
-  const int n = *rc.n;
-  for (long long w = blockIdx.x; w < (long long)n * shares; w += gridDim.x) {
-    const int i = (int)(w / shares), sh = (int)(w - (long long)i * shares);
-    const int t = rc.tok[i], e = sh * kShare + warp;
-    const uint32_t* mask = rc.mask + (size_t)i * 32;
-    if (e < N && ((mask[e & 31] >> (e >> 5)) & 1u)) {
+    int32_t* __restrict__ counts, float* __restrict__ logits, const int32_t* __restrict__ n_listed,
+    const int32_t* __restrict__ listed) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ double part[MAXT / 32][kDots];
+  __shared__ double red[33];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = r.N_r, nv = d / 8;
+  const BlockRoute b = block_route_smem(smem_raw, N, r.K);
+  const int n = listed ? *n_listed : T;
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int t = listed ? listed[i] : i;
+    double a = 0.0, mag = 0.0;
+    if (tid < N) {
+      const size_t at = (size_t)t * ld + tid, stride = (size_t)T * ld;
+      for (int s = 0; s < S; ++s) {
+        const double v = EXACT ? static_cast<const double*>(P)[at + s * stride]
+                               : (double)static_cast<const float*>(P)[at + s * stride];
+        a += v;
+        mag += fabs(v);
+      }
+      // float32 slices: the logit rounded once, as the first pass saw it
+      if (!EXACT) a = (double)(float)a;
+      if (logits) logits[(size_t)t * N + tid] = (float)a;
+    }
+    float logit_err = 0.f;
+    if (!EXACT) {
+      mag = block_reduce(mag, false, red);
+      logit_err = mag == 0.0 ? 0.f : kLogitError * fmaxf(4.f, (float)mag);
+    }
+    if (tid < N) {
+      b.x[tid] = a;
+      b.exact_f[tid] = EXACT || mag == 0.0;
+    }
+    const auto fetch = [&](int nl) {
       const uint4* ur = reinterpret_cast<const uint4*>(u + (size_t)t * d);
-      const uint4* er = reinterpret_cast<const uint4*>(E + (size_t)e * d);
-      double a = 0.0, b = 0.0;
-      constexpr int U = 4;
-      for (int v0 = lane; v0 < nv; v0 += 32 * U) {
-        uint4 x[U], y[U];
+      for (int c0 = 0; c0 < nl; c0 += kDots) {
+        const int nc = min(kDots, nl - c0);
+        double acc[kDots];
 #pragma unroll
-        for (int q = 0; q < U; ++q) {
-          const int v = v0 + 32 * q;
-          x[q] = v < nv ? ur[v] : make_uint4(0, 0, 0, 0);
-          y[q] = v < nv ? er[v] : make_uint4(0, 0, 0, 0);
-        }
+        for (int c = 0; c < kDots; ++c) acc[c] = 0.0;
+        for (int v = tid; v < nv; v += blockDim.x) {
+          float fx[8];
+          Vec<__nv_bfloat16>::load(__ldg(ur + v), fx);
+          uint4 y[kDots];
 #pragma unroll
-        for (int q = 0; q < U; ++q) {
-          float fx[8], fy[8];
-          Vec<__nv_bfloat16>::load(x[q], fx);
-          Vec<__nv_bfloat16>::load(y[q], fy);
+          for (int c = 0; c < kDots; ++c)
+            y[c] = c < nc
+                       ? __ldg(reinterpret_cast<const uint4*>(E + (size_t)b.list[c0 + c] * d) + v)
+                       : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int k = 0; k < 8; k += 2) {
-            a += (double)(fx[k] * fy[k]);
-            b += (double)(fx[k + 1] * fy[k + 1]);
+          for (int c = 0; c < kDots; ++c) {
+            if (c < nc) {
+              float fy[8];
+              Vec<__nv_bfloat16>::load(y[c], fy);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) acc[c] += (double)(fx[k] * fy[k]);
+            }
           }
         }
-      }
-      a = sel_warp_sum(a + b);
-      if (lane == 0) rc.x[(size_t)i * N + e] = a;
-    }
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(&rc.done[i], 1) == shares - 1;
-    __syncthreads();
-    if (last && warp == 0) {
-      __threadfence();
-      const float* row = P + (size_t)t * ld;
-      const size_t stride = (size_t)T * ld;
-      const auto getx = [&](int q) {
-        if ((mask[q & 31] >> (q >> 5)) & 1u) return __ldcg(rc.x + (size_t)i * N + q);
-        double a = 0.0;
-        for (int s = 0; s < S; ++s) a += (double)row[s * stride + q];
-        return (double)(float)a;
-      };
-      double x[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int q = j * 32 + lane;
-        x[j] = q < N ? getx(q) : 0.0;
+        for (int c = 0; c < kDots; ++c) {
+          if (c < nc) {
+            const double v = sel_warp_sum(acc[c]);
+            if (lane == 0) part[warp][c] = v;
+          }
+        }
+        __syncthreads();
+        if (tid < nc) {
+          double v = 0.0;
+          for (int w = 0; w < (int)(blockDim.x >> 5); ++w) v += part[w][tid];
+          b.x[b.list[c0 + tid]] = v;
+        }
+        __syncthreads();
       }
-      int32_t* ti = idx + (size_t)t * r.K;
-      for (int k = lane; k < r.K; k += 32) atomicSub(&counts[ti[k]], 1);
-      select_token<V, double>(x, getx, bias, r, 0.f, wk, ti, gate + (size_t)t * r.K);
-      for (int k = lane; k < r.K; k += 32) atomicAdd(&counts[ti[k]], 1);
-    }
+    };
+    block_route(b, r, bias, logit_err, fetch, idx + (size_t)t * r.K, gate + (size_t)t * r.K,
+                counts);
     __syncthreads();
   }
 }
@@ -622,14 +600,10 @@ size_t tc_ws_bytes(int T, int d, int N, Recheck* rc, uint8_t* base) {
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes, 256); return at; };
   take((size_t)L.S * T * L.ld * 4);
-  const size_t n = take(4), tok = take((size_t)T * 4), mask = take((size_t)T * 128),
-               done = take((size_t)T * 4), x = take((size_t)T * N * 8);
+  const size_t n = take(4), tok = take((size_t)T * 4);
   if (rc) {
     rc->n = reinterpret_cast<int32_t*>(base + n);
     rc->tok = reinterpret_cast<int32_t*>(base + tok);
-    rc->mask = reinterpret_cast<uint32_t*>(base + mask);
-    rc->done = reinterpret_cast<int32_t*>(base + done);
-    rc->x = reinterpret_cast<double*>(base + x);
   }
   return o;
 }
@@ -685,6 +659,33 @@ size_t route_scored_ws_bytes(int T, int d, int N_r) {
   return a > b ? a : b;
 }
 
+// Tokens up to which the block path routes every token: a block per token
+// keeps a lone token's latency low, a warp per token costs a third of the
+// instructions.
+constexpr int kBlockTokens = 1024;
+
+namespace {
+template <bool EXACT>
+moe_status launch_router_token(const void* u, const void* E, const void* P, int S, int ld,
+                               const float* b, int T, int d, const SelectRule& r, int32_t* idx,
+                               float* gate, int32_t* counts, float* logits,
+                               const int32_t* n_listed, const int32_t* listed, int blocks,
+                               cudaStream_t s) {
+  int threads = (r.N_r + 31) / 32 * 32;
+  if (threads < 128) threads = 128;
+  const size_t smem = block_route_bytes(r.N_r, r.K);
+  const auto ub = static_cast<const __nv_bfloat16*>(u);
+  const auto eb = static_cast<const __nv_bfloat16*>(E);
+  if (threads <= 256)
+    router_token_kernel<EXACT, 256><<<blocks, threads, smem, s>>>(
+        ub, eb, P, S, ld, b, T, d, r, idx, gate, counts, logits, n_listed, listed);
+  else
+    router_token_kernel<EXACT, 1024><<<blocks, threads, smem, s>>>(
+        ub, eb, P, S, ld, b, T, d, r, idx, gate, counts, logits, n_listed, listed);
+  return cuda_check(cudaGetLastError(), "router_token launch");
+}
+}  // namespace
+
 moe_status launch_route_scored(const void* u, const void* E, moe_dtype dt, const float* b, int T,
                                int d, int N_r, int K, int score, int n_groups, int topk_groups,
                                int group_top, int renorm, float gate_scale, int32_t* idx,
@@ -693,12 +694,6 @@ moe_status launch_route_scored(const void* u, const void* E, moe_dtype dt, const
   using bf = __nv_bfloat16;
   const SelectRule r{N_r, K, score, n_groups, topk_groups, group_top, renorm, gate_scale};
   moe_status st;
-  const int V = dispatch_v(N_r);
-  // warps per block of the selection: one while that fills no SM twice
-  const int wpb = T <= 2 * sm_count() ? 1 : 4;
-  int blocks = (T + wpb - 1) / wpb;
-  if (blocks > 16 * sm_count()) blocks = 16 * sm_count();
-  const size_t smem = (size_t)N_r * sizeof(int) * (1 + wpb);
   if (dt == MOE_BF16 && T > kFewTokens) {
     float* P = static_cast<float*>(ws);
     Recheck rc;
@@ -706,25 +701,25 @@ moe_status launch_route_scored(const void* u, const void* E, moe_dtype dt, const
     const LogitTiling L = logit_tiling(T, d, N_r);
     st = launch_logits_tc(u, E, T, d, N_r, P, counts, rc.n, s);
     if (st != MOE_OK) return st;
+    if (T <= kBlockTokens)
+      return launch_router_token<false>(u, E, P, L.S, L.ld, b, T, d, r, idx, gate, counts, logits,
+                                        nullptr, nullptr, T, s);
+    const int wpb = 4, blocks = (T + wpb - 1) / wpb < 16 * sm_count() ? (T + wpb - 1) / wpb
+                                                                      : 16 * sm_count();
+    const size_t smem = (size_t)N_r * sizeof(int) * (1 + wpb);
 #define MOE_SELECT(v)                                                                        \
   case v:                                                                                    \
     router_select_kernel<v><<<blocks, wpb * 32, smem, s>>>(P, L.S, L.ld, b, T, r, idx, gate, \
                                                            counts, logits, rc);              \
     break;
-    switch (V) { MOE_SELECT(1) MOE_SELECT(2) MOE_SELECT(4) MOE_SELECT(8) MOE_SELECT(16) MOE_SELECT(32) }
+    switch (dispatch_v(N_r)) {
+      MOE_SELECT(1) MOE_SELECT(2) MOE_SELECT(4) MOE_SELECT(8) MOE_SELECT(16) MOE_SELECT(32)
+    }
 #undef MOE_SELECT
     st = cuda_check(cudaGetLastError(), "router_select launch");
     if (st != MOE_OK) return st;
-    const int rblocks = 4 * sm_count();
-#define MOE_RECHECK(v)                                                                       \
-  case v:                                                                                    \
-    router_recheck_kernel<v><<<rblocks, 32 * kShare, N_r * sizeof(float), s>>>(              \
-        static_cast<const bf*>(u), static_cast<const bf*>(E), P, L.S, L.ld, b, T, d, r, idx, \
-        gate, counts, rc);                                                                   \
-    break;
-    switch (V) { MOE_RECHECK(1) MOE_RECHECK(2) MOE_RECHECK(4) MOE_RECHECK(8) MOE_RECHECK(16) MOE_RECHECK(32) }
-#undef MOE_RECHECK
-    return cuda_check(cudaGetLastError(), "router_recheck launch");
+    return launch_router_token<false>(u, E, P, L.S, L.ld, b, T, d, r, idx, gate, counts, nullptr,
+                                      rc.n, rc.tok, 2 * sm_count(), s);
   }
   double* P = static_cast<double*>(ws);
   int S = 1;
@@ -744,14 +739,9 @@ moe_status launch_route_scored(const void* u, const void* E, moe_dtype dt, const
   }
   st = cuda_check(cudaGetLastError(), "router float64 logits launch");
   if (st != MOE_OK) return st;
-#define MOE_SELECT64(v)                                                                      \
-  case v:                                                                                    \
-    router_select64_kernel<v><<<blocks, wpb * 32, smem, s>>>(P, S, N_r, b, T, r, idx, gate,  \
-                                                             counts, logits);                \
-    break;
-  switch (V) { MOE_SELECT64(1) MOE_SELECT64(2) MOE_SELECT64(4) MOE_SELECT64(8) MOE_SELECT64(16) MOE_SELECT64(32) }
-#undef MOE_SELECT64
-  return cuda_check(cudaGetLastError(), "router_select64 launch");
+  const int blocks = T < 16 * sm_count() ? T : 16 * sm_count();
+  return launch_router_token<true>(u, E, P, S, N_r, b, T, d, r, idx, gate, counts, logits, nullptr,
+                                   nullptr, blocks, s);
 }
 
 }  // namespace moe

@@ -1,4 +1,4 @@
-// One token's scored routing by one warp (moe_route_scored): scores of every
+// One token's scored routing (moe_route_scored), by a warp or by a block: scores of every
 // expert from its logit row, the K largest keys f32(score) + bias, optionally
 // inside the best expert groups, and the gates.
 //
@@ -6,15 +6,20 @@
 //   key_i = f32(s_i) + b_i;  a group's score is the sum of its group_top largest keys
 //   gate_k = scale * s_k  or  scale * s_k / sum of the selected s
 //
-// X = double: the row holds exact logits (float64 sums of products), every
-// score is float64 and rounded once, so the keys are the definition's.
-// X = float: the row holds float32 logits; a token with a decision closer than
-// the float32 error bound below is listed for the exact pass.
-//
-// Lane l holds experts j*32 + l (j < V).  Order: key descending, lower index
+// Warp: lane l holds experts j*32 + l (j < V) and K rounds of an arg-max pick
+// the experts (fewest instructions: many tokens).  Block: a thread per expert
+// counts the keys before its own, which is its place in the order (no rounds
+// and little code to fetch: few tokens, and the exact pass).  Order: key descending, lower index
 // first on equal keys, a NaN key before every number.  Experts outside the
 // kept groups are never selected; one whose key is -inf (b = -inf) is selected
 // only when the kept groups hold fewer than K others.
+//
+// Exactness.  A token is first selected from float32 keys.  A decision (two
+// neighbours in the order, the last kept against the best excluded group)
+// whose gap is inside the keys' error bound is open; the experts that can take
+// part in it get their exact key (float64 logit and score, rounded once) and
+// the token is selected again, until no decision is open.  Equal exact keys
+// are ties of the definition.
 #pragma once
 
 #include <math.h>
@@ -27,14 +32,13 @@ namespace moe {
 __device__ __forceinline__ uint32_t sel_ord(float f) {
   if (f != f) return 0xffffffffu;
   const uint32_t b = __float_as_uint(f + 0.0f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float sel_val(uint32_t o) {
+  if (o == 0xffffffffu) return NAN;
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
-// e^x for the scores: float64 in the exact pass; float32 with expf, whose
-// error (2 ulp) the listing bound counts.
 __device__ __forceinline__ float sel_exp(float x) { return expf(x); }
 __device__ __forceinline__ double sel_exp(double x) { return exp(x); }
 
@@ -65,205 +69,457 @@ struct SelectRule {
   float scale;
 };
 
-// Listing bound.  The tensor-core logits (chunks of at most 32 accumulation
-// steps, joined in float32 round-to-nearest) stay within kLogitError of the
-// exact ones per unit of logit magnitude: measured over N(0,1) rows at
-// d = 7168 the largest error is 1.6e-6 at max|x| = 5, and the bound below
-// leaves six times that.
+// Bound on a float32 logit's error per unit of max(4, largest |logit|).  The
+// tensor-core sums are cut every 32 accumulation steps; over N(0,1) rows at
+// d = 7168 and 2048 their largest error is 1.6e-6 (kLogitError * 4 = 1e-5).
 constexpr float kLogitError = 2.5e-6f;
 
-// What the float32 pass says about a token: whether a decision was closer than
-// its error bound, and per lane the mask of the experts (bit j: j*32 + lane)
-// whose exact keys can take part in it.
-struct CloseCall {
-  bool close;
-  uint32_t mask;
+// Per token: the softmax's largest logit and sum, and the error bound of its
+// float32 keys: |key error| <= err + kKeyRounding |key|.
+struct TokenScale {
+  float m, z, err;
 };
+constexpr float kKeyRounding = 1.2e-7f;
 
-// wk: this warp's N_r floats of shared memory (used under a group limit).
-// x[j]: the lane's logits, getx(e): the logit of any expert; absmax: the
-// row's largest |logit|, summed over its slices' magnitudes (X = float).
-// Writes the token's idx and gate.
-template <int V, typename X, typename GetX>
-__device__ __forceinline__ CloseCall select_token(const X (&x)[V], GetX getx,
-                                                  const float* __restrict__ bias,
-                                                  const SelectRule& r, float absmax, float* wk,
-                                                  int32_t* __restrict__ idx,
-                                                  float* __restrict__ gate) {
-  constexpr bool kExact = sizeof(X) == 8;
+// Float32 keys and scores of a row of float32 logits.  logit_err: bound on
+// their error.  d s = s(1-s) dx (sigmoid), at most 2 s(1-s) max|dx| (softmax);
+// the fast exponential and division cost a score of size s at most 8 * 2^-23 s
+// (the exponential's argument error, |x| 2^-23, is weighted by s(1-s) or by
+// s ln(smax / s) < 0.4 smax).
+template <int V>
+__device__ __forceinline__ TokenScale select_keys(const float (&x)[V], const float* bias,
+                                                  const SelectRule& r, float logit_err,
+                                                  float (&sc)[V], float (&key)[V]) {
   const int lane = threadIdx.x & 31, N = r.N_r;
+  TokenScale ts{0.f, 1.f, 0.f};
   const bool softmax = r.score == MOE_SCORE_SOFTMAX;
-  X m = X(0), inv = X(1);
+  if (logit_err == 0.f) {
+    // a row of exact zeros (a padding token): every score is 1/2, or 1/N_r
+    const float s0 = softmax ? 1.f / (float)N : 0.5f;
+    ts.z = (float)N;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int e = j * 32 + lane;
+      sc[j] = e < N ? s0 : 0.f;
+      key[j] = e < N ? (bias ? s0 + bias[e] : s0) : -INFINITY;
+    }
+    return ts;
+  }
   if (softmax) {
-    m = -INFINITY;
+    float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (j * 32 + lane < N) m = x[j] > m || x[j] != x[j] ? x[j] : m;
-    m = sel_warp_max(m);
-    X z = X(0);
+    ts.m = sel_warp_max(m);
+    float z = 0.f;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (j * 32 + lane < N) z += sel_exp(x[j] - m);
-    inv = sel_warp_sum(z);
+    for (int j = 0; j < V; ++j) {
+      sc[j] = j * 32 + lane < N ? __expf(x[j] - ts.m) : 0.f;
+      z += sc[j];
+    }
+    ts.z = sel_warp_sum(z);
+    const float inv = __fdividef(1.f, ts.z);
+#pragma unroll
+    for (int j = 0; j < V; ++j) sc[j] *= inv;
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float e = __expf(x[j] < 0.f ? x[j] : -x[j]);
+      sc[j] = j * 32 + lane < N ? __fdividef(x[j] < 0.f ? e : 1.f, 1.f + e) : 0.f;
+    }
   }
-  float key[V];
-  float wmax = 0.f, smax = 0.f;
+  float w = 0.f, s = 0.f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int e = j * 32 + lane;
-    key[j] = -INFINITY;
-    if (e < N) {
-      const float s = softmax ? (float)(sel_exp(x[j] - m) / inv) : (float)sel_sigmoid(x[j]);
-      key[j] = bias ? s + bias[e] : s;
-      if (!kExact) {
-        wmax = fmaxf(wmax, s * (1.f - s));
-        smax = fmaxf(smax, s);
-      }
-    }
+    key[j] = e < N ? (bias ? sc[j] + bias[e] : sc[j]) : -INFINITY;
+    w = fmaxf(w, sc[j] * (1.f - sc[j]));
+    s = fmaxf(s, sc[j]);
   }
-  // |key error| <= err + 2^-23 |key|: d s = s(1-s) dx (sigmoid), at most
-  // 2 s(1-s) max|dx| (softmax), and the scores' own rounding.  A row of exact
-  // zeros (a padding token) has exact scores.
-  float err = 0.f, rel = 0.f;
-  if (!kExact && absmax != 0.f) {
-    wmax = sel_warp_max(wmax);
-    smax = sel_warp_max(smax);
-    err = kLogitError * fmaxf(4.f, absmax) * wmax * (softmax ? 2.f : 1.f) + 4.8e-7f * smax;
-    rel = 2.4e-7f;
-  }
-  bool group_close = false;
+  // non-negative floats compare as integers
+  w = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(w)));
+  s = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s)));
+  ts.err = logit_err * w * (softmax ? 2.f : 1.f) + 9.6e-7f * s;
+  return ts;
+}
+
+// What a warp's selection decided: lane k's expert of slot k (k < 32; every
+// slot is in idx), and whether a decision is open.
+struct Selection {
+  int e;
+  bool open;
+};
+
+// key: this lane's keys, off by at most err + kKeyRounding |key| (err == 0:
+// exact).  wk: N_r floats of shared memory for this warp.
+template <int V>
+__device__ __forceinline__ Selection select_core(const float (&key)[V], float err,
+                                                 const SelectRule& r, float* wk,
+                                                 int32_t* __restrict__ idx) {
+  const int lane = threadIdx.x & 31, N = r.N_r;
+  const float rel = err > 0.f ? kKeyRounding : 0.f;
+  Selection out{0, false};
   uint32_t ko[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) ko[j] = j * 32 + lane < N ? sel_ord(key[j]) : 0u;
   if (r.topk_groups < r.n_groups) {
     const int gs = N / r.n_groups;
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (j * 32 + lane < N) wk[j * 32 + lane] = key[j];
-    __syncwarp();
-    // lane g: the score of group g, its largest or its two largest keys
-    uint32_t go = 0u;
-    if (lane < r.n_groups) {
+    // e / gs as a product: exact while e < 1024 and e * gs < 2^22
+    const uint32_t inv_gs = ((1u << 22) + gs - 1) / gs;
+    const bool two = r.group_top == 2;
+    uint32_t ga = 0u, gb = 0u;                      // lane g: the largest keys of group g
+    if (gs % 32 == 0) {
+      const int per = gs / 32;                      // a group is `per` whole rows of lanes
       uint32_t a = 0u, b = 0u;
-      for (int i = 0, at = lane < gs ? lane : 0; i < gs; ++i) {   // banks spread over the lanes
-        const uint32_t o = sel_ord(wk[lane * gs + at]);
-        if (o > a) { b = a; a = o; } else if (o > b) b = o;
-        if (++at == gs) at = 0;
+      int left = per, g = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (j * 32 < N) {
+          b = max(b, min(a, ko[j]));
+          a = max(a, ko[j]);
+          if (--left == 0) {
+            const uint32_t m1 = __reduce_max_sync(0xffffffffu, a);
+            uint32_t m2 = 0u;
+            if (two) {
+              // one holder of the largest key steps back to its second
+              const int who = __ffs(__ballot_sync(0xffffffffu, a == m1)) - 1;
+              m2 = __reduce_max_sync(0xffffffffu, lane == who ? b : a);
+            }
+            if (lane == g) { ga = m1; gb = m2; }
+            a = b = 0u;
+            left = per;
+            ++g;
+          }
+        }
       }
-      float sc = sel_val(a);
-      if (a == 0xffffffffu) sc = NAN;
-      if (r.group_top == 2) sc = sc + (b == 0xffffffffu ? NAN : sel_val(b));
-      go = sel_ord(sc);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (j * 32 + lane < N) wk[j * 32 + lane] = key[j];
+      __syncwarp();
+      if (lane < r.n_groups) {
+        for (int i = 0, at = lane < gs ? lane : 0; i < gs; ++i) {   // banks spread over the lanes
+          const uint32_t o = sel_ord(wk[lane * gs + at]);
+          gb = max(gb, min(ga, o));
+          ga = max(ga, o);
+          if (++at == gs) at = 0;
+        }
+      }
+      __syncwarp();
     }
-    __syncwarp();
+    uint32_t go = 0u;
+    if (lane < r.n_groups) go = sel_ord(two ? sel_val(ga) + sel_val(gb) : sel_val(ga));
     unsigned kept = 0;
     float last = INFINITY;
     for (int k = 0; k <= r.topk_groups; ++k) {       // one more round: the best group left out
       const uint32_t mx = __reduce_max_sync(0xffffffffu, go);
-      const int bg = __reduce_min_sync(0xffffffffu, go == mx && mx ? lane : 32);
       if (mx == 0u) break;
-      const float v = mx == 0xffffffffu ? NAN : sel_val(mx);
+      const int bg = __ffs(__ballot_sync(0xffffffffu, go == mx)) - 1;
+      const float v = sel_val(mx);
       if (k < r.topk_groups) {
         kept |= 1u << bg;
         last = v;
         if (lane == bg) go = 0u;
       } else {
-        group_close = last - v < r.group_top * 2.f * err + rel * (fabsf(last) + fabsf(v));
+        out.open = last - v < 2.f * r.group_top * err + rel * (fabsf(last) + fabsf(v));
       }
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int e = j * 32 + lane;
-      if (e < N && !((kept >> (e / gs)) & 1u)) ko[j] = 0u;
+      const uint32_t e = j * 32 + lane;
+      if (e < (uint32_t)N && !((kept >> (e * inv_gs >> 22)) & 1u)) ko[j] = 0u;
     }
   }
-  // K rounds of a warp arg-max; lane k % 32 keeps and writes winner k
-  float lo = INFINITY, hi = -INFINITY, prev = INFINITY;
-  int my_e = 0;
-  for (int k = 0; k < r.K; ++k) {
-    uint32_t lb = 0u;
+  // K rounds of a warp arg-max, and one more for the best expert left out;
+  // lane k % 32 keeps and writes winner k
+  float prev = INFINITY;
+  for (int k = 0; k <= r.K; ++k) {
+    uint32_t lb = ko[0];
     int lj = 0;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
+    for (int j = 1; j < V; ++j)
       if (ko[j] > lb) { lb = ko[j]; lj = j; }
     const uint32_t mx = __reduce_max_sync(0xffffffffu, lb);
+    if (mx == 0u) break;                             // nothing eligible is left
     const int be = __reduce_min_sync(0xffffffffu, lb == mx ? lj * 32 + lane : 0x7fffffff);
-    if (!kExact) {
-      const float v = mx == 0xffffffffu ? NAN : sel_val(mx);
-      if (prev - v < 2.f * err + rel * (fabsf(prev) + fabsf(v))) {
-        lo = fminf(lo, v);
-        hi = fmaxf(hi, prev);
-      }
-      prev = v;
-    }
+    const float v = sel_val(mx);
+    if (prev - v < 2.f * err + rel * (fabsf(prev) + fabsf(v))) out.open = true;
+    prev = v;
+    if (k == r.K) break;
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (j * 32 + lane == be) ko[j] = 0u;
     if (lane == (k & 31)) {
-      my_e = be;
+      out.e = be;
       idx[k] = be;
     }
   }
-  // gates: lane k takes slots k, k + 32, ... (it wrote their idx itself)
-  const auto slot_x = [&](int k) { return getx(r.K <= 32 ? my_e : idx[k]); };
-  if (!r.renorm) {
-    for (int k = lane; k < r.K; k += 32) {
-      const X xk = slot_x(k);
-      const X s = softmax ? sel_exp(xk - m) / inv : sel_sigmoid(xk);
-      gate[k] = (float)(s * (X)r.scale);
+  return out;
+}
+
+// Gates of the selected experts from their logits (X: float or float64); m, z:
+// the softmax's largest logit and sum.
+template <int V, typename X>
+__device__ __forceinline__ void select_gates(const X (&x)[V], int my_e, X m, X z,
+                                             const SelectRule& r, const int32_t* idx,
+                                             float* __restrict__ gate) {
+  const int lane = threadIdx.x & 31;
+  const bool softmax = r.score == MOE_SCORE_SOFTMAX;
+  // the logit of slot k0 + lane (0 past the last slot); every lane takes part
+  const auto slot_x = [&](int k0) {
+    const int e = k0 + lane < r.K ? (r.K <= 32 ? my_e : idx[k0 + lane]) : 0;
+    X v = X(0);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const X w = __shfl_sync(0xffffffffu, x[j], e & 31);
+      if (j == (e >> 5)) v = w;
     }
-  } else {
-    // scores relative to the largest selected one, so that their sum cannot
-    // underflow: e^(x - xm), or s(x) / s(xm) of sigmoids (e^(x - xm) to
-    // e^-30 where xm < -30)
-    X xm = -INFINITY;
-    for (int k = lane; k < r.K; k += 32) {
-      const X xk = slot_x(k);
-      xm = xk > xm || xk != xk ? xk : xm;
+    return v;
+  };
+  if (!r.renorm) {
+    for (int k0 = 0; k0 < r.K; k0 += 32) {
+      const X xk = slot_x(k0);
+      const X s = softmax ? sel_exp(xk - m) / z : sel_sigmoid(xk);
+      if (k0 + lane < r.K) gate[k0 + lane] = (float)(s * (X)r.scale);
+    }
+    return;
+  }
+  // scores relative to the largest selected one, so that their sum cannot
+  // underflow: e^(x - xm), or s(x) / s(xm) of sigmoids (e^(x - xm), right to
+  // e^-30, where xm < -30)
+  X xm = -INFINITY;
+  for (int k0 = 0; k0 < r.K; k0 += 32) {
+    const X xk = slot_x(k0);
+    if (k0 + lane < r.K) xm = xk > xm || xk != xk ? xk : xm;
+  }
+  xm = sel_warp_max(xm);
+  const bool ratio = !softmax && !(xm < X(-30));
+  const X sm = ratio ? sel_sigmoid(xm) : X(1);
+  X sum = X(0), w = X(0);
+  for (int k0 = 0; k0 < r.K; k0 += 32) {
+    const X xk = slot_x(k0);
+    w = ratio ? sel_sigmoid(xk) / sm : sel_exp(xk - xm);
+    if (k0 + lane < r.K) sum += w;
+  }
+  sum = sel_warp_sum(sum);
+  for (int k0 = 0; k0 < r.K; k0 += 32) {
+    if (r.K > 32) {
+      const X xk = slot_x(k0);
+      w = ratio ? sel_sigmoid(xk) / sm : sel_exp(xk - xm);
+    }
+    if (k0 + lane < r.K) gate[k0 + lane] = (float)(w / sum * (X)r.scale);
+  }
+}
+
+// ---------------------------------------------------------------- by a block
+// Shared memory of the block path, for N experts and K slots.
+struct BlockRoute {
+  double* x;          // [N] logits: exact, or float32 ones where exact_f is 0
+  uint32_t* ord;      // [N + 3] keys in order form (0: not eligible)
+  float* top_key;     // [K + 1] keys in order, the best one left out last
+  uint16_t* top_id;   // [K + 1] their experts
+  uint16_t* list;     // [N] experts whose exact logit is wanted
+  uint8_t* exact_f;   // [N]
+};
+__host__ __device__ inline size_t block_route_bytes(int N, int K) {
+  return (size_t)N * 8 + ((size_t)N + 4) * 4 + ((size_t)K + 2) * 8 + (size_t)N * 2 + N + 16;
+}
+__device__ __forceinline__ BlockRoute block_route_smem(uint8_t* p, int N, int K) {
+  BlockRoute b;
+  b.x = reinterpret_cast<double*>(p);
+  b.ord = reinterpret_cast<uint32_t*>(p + (size_t)((N + 1) / 2 * 2) * 8);   // 16-byte aligned
+  b.top_key = reinterpret_cast<float*>(b.ord + (N + 3) / 4 * 4);
+  b.top_id = reinterpret_cast<uint16_t*>(b.top_key + K + 1);
+  b.list = b.top_id + K + 1;
+  b.exact_f = reinterpret_cast<uint8_t*>(b.list + N);
+  return b;
+}
+
+// Sum or largest of v over the block, in warp order (red: 33 doubles).
+__device__ __forceinline__ double block_reduce(double v, bool sum, double* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  v = sum ? sel_warp_sum(v) : sel_warp_max(v);
+  __syncthreads();
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  v = lane < nw ? red[lane] : (sum ? 0.0 : -(double)INFINITY);
+  return sum ? sel_warp_sum(v) : sel_warp_max(v);
+}
+
+// Routes one token by the whole block (blockDim.x >= N, whole warps), from
+// b.x and b.exact_f; logit_err bounds the error of the inexact logits.
+// fetch(n): fills b.x for the experts b.list[0, n) with their exact logits and
+// synchronises the block.  Its last reads of b are warp 0's: the caller
+// synchronises before it fills b again.
+template <typename Fetch>
+__device__ __forceinline__ void block_route(const BlockRoute& b, const SelectRule& r,
+                                            const float* __restrict__ bias, float logit_err,
+                                            Fetch fetch, int32_t* __restrict__ idx,
+                                            float* __restrict__ gate,
+                                            int32_t* __restrict__ counts) {
+  __shared__ double red[33];
+  __shared__ float gkey[32][2];
+  __shared__ unsigned s_near;
+  __shared__ int n_list, s_lo, s_hi;
+  const int e = threadIdx.x, N = r.N_r, K = r.K, lane = e & 31;
+  const bool softmax = r.score == MOE_SCORE_SOFTMAX, mine = e < N;
+  const bool grouped = r.topk_groups < r.n_groups, two = r.group_top == 2;
+  const int gs = N / r.n_groups, g = mine ? e / gs : 0;
+  const float bi = bias && mine ? bias[e] : 0.f;
+  double m = 0.0, z = 1.0;
+  while (true) {
+    __syncthreads();
+    const bool ex = mine && b.exact_f[e];
+    const bool all = __syncthreads_and(!mine || ex);
+    const double x = mine ? b.x[e] : 0.0;
+    if (softmax) {
+      m = block_reduce(mine ? x : -(double)INFINITY, false, red);
+      z = block_reduce(mine ? exp(x - m) : 0.0, true, red);
+    }
+    const float s = mine ? (float)(softmax ? exp(x - m) / z : sel_sigmoid(x)) : 0.f;
+    const float key = bias ? s + bi : s;
+    // error of the inexact keys, and of the softmax's sum, which exact keys share
+    float err = 0.f, eta = 0.f, smax = 0.f;
+    if (!all) {
+      const float w = (float)block_reduce((double)(s * (1.f - s)), false, red);
+      smax = (float)block_reduce((double)s, false, red);
+      err = logit_err * w * (softmax ? 2.f : 1.f) + 1.2e-7f * smax;
+      eta = softmax ? logit_err : 0.f;
+    }
+    const float rel = err > 0.f ? kKeyRounding : 0.f;
+    uint32_t o = mine ? sel_ord(key) : 0u;
+    if (mine) b.ord[e] = o;
+    if (e == 0) { n_list = 0; s_lo = 0x7fffffff; s_hi = -1; s_near = 0u; }
+    if (e < 32) gkey[e][0] = gkey[e][1] = 0.f;
+    __syncthreads();
+    bool want = false, z_open = false;
+    if (grouped) {
+      // place inside the group; the first one or two make its score
+      int place = 0;
+      if (mine)
+        for (int i = g * gs; i < g * gs + gs; ++i) {
+          const uint32_t v = b.ord[i];
+          place += v > o || (v == o && i < e);
+        }
+      if (mine && place < 2) gkey[g][place] = key;
+      __syncthreads();
+      const float need = gkey[g][two ? 1 : 0];       // the last key the group's score counts
+      const bool near = mine && !ex && key >= need - 2.f * err - 2.f * rel * fabsf(need);
+      if (near) atomicOr(&s_near, 1u << g);
+      __syncthreads();
+      // groups: lane q of every warp holds group q
+      const bool has = lane < r.n_groups;
+      const float gsc = has ? (two ? gkey[lane][0] + gkey[lane][1] : gkey[lane][0]) : 0.f;
+      const uint32_t go = has ? sel_ord(gsc) : 0u;
+      const float ge = has && ((s_near >> lane) & 1u) ? r.group_top * err + rel * fabsf(gsc) : 0.f;
+      int before = 0;
+      for (int q = 0; q < r.n_groups; ++q) {
+        const uint32_t v = __shfl_sync(0xffffffffu, go, q);
+        before += v > go || (v == go && q < lane);
+      }
+      const unsigned kept = __ballot_sync(0xffffffffu, has && before < r.topk_groups);
+      const int at_last = __ffs(__ballot_sync(0xffffffffu, has && before == r.topk_groups - 1)) - 1;
+      const int at_next = __ffs(__ballot_sync(0xffffffffu, has && before == r.topk_groups)) - 1;
+      const float last = __shfl_sync(0xffffffffu, gsc, at_last);
+      const float next = __shfl_sync(0xffffffffu, gsc, at_next);
+      const float emax = sel_warp_max(ge);
+      if (last - next < 2.f * emax) {
+        // the members that can enter the scores of the groups near the border
+        const float mine_sc = two ? gkey[g][0] + gkey[g][1] : gkey[g][0];
+        want = near && mine_sc >= next - 4.f * emax && mine_sc <= last + 4.f * emax;
+      }
+      if (eta > 0.f && last - next <= 4.f * eta * smax + 2.f * kKeyRounding * fabsf(last) &&
+          !(last - next < 2.f * emax))
+        z_open = true;
+      if (mine && !((kept >> g) & 1u)) o = 0u;
+      __syncthreads();                               // every thread has read ord for its place
+      if (mine) b.ord[e] = o;
+      __syncthreads();
+    }
+    // place in the order: how many eligible keys come before
+    int place = 0;
+    if (mine && o != 0u) {
+      const uint4* ov = reinterpret_cast<const uint4*>(b.ord);
+      const int n4 = N / 4;
+      int i = 0;
+#pragma unroll 4
+      for (; i < n4; ++i) {
+        const uint4 v = ov[i];
+        place += (v.x > o || (v.x == o && 4 * i < e)) + (v.y > o || (v.y == o && 4 * i + 1 < e)) +
+                 (v.z > o || (v.z == o && 4 * i + 2 < e)) + (v.w > o || (v.w == o && 4 * i + 3 < e));
+      }
+      for (int k = 4 * n4; k < N; ++k) {
+        const uint32_t v = b.ord[k];
+        place += v > o || (v == o && k < e);
+      }
+    }
+    const bool placed = mine && o != 0u && place <= K;
+    if (placed) {
+      b.top_key[place] = key;
+      b.top_id[place] = (uint16_t)e;
+    }
+    const int n_top = __syncthreads_count(placed);   // K + 1, or K where no other is eligible
+    bool open = false;
+    if (!all) {
+      for (int k = e; k + 1 < n_top; k += blockDim.x) {
+        const float a = b.top_key[k], c = b.top_key[k + 1];
+        if (b.exact_f[b.top_id[k]] && b.exact_f[b.top_id[k + 1]]) {
+          // only the softmax's sum is left to tell them apart
+          const float sa = bias ? a - bias[b.top_id[k]] : a, sb = bias ? c - bias[b.top_id[k + 1]] : c;
+          if (eta > 0.f && a - c <= eta * fabsf(sa - sb) + 2.f * kKeyRounding * fmaxf(fabsf(a), fabsf(c)))
+            z_open = true;
+        } else if (a - c < 2.f * err + rel * (fabsf(a) + fabsf(c))) {
+          atomicMin(&s_lo, k + 1);                   // places between which the open pairs lie
+          atomicMax(&s_hi, k + 1);
+        }
+      }
+      z_open = __syncthreads_or(z_open);
+      if (s_hi >= 0 && mine && !ex) {
+        const float lo = b.top_key[s_hi], hi = b.top_key[s_lo - 1];
+        const float pad = 3.f * err + 2.f * rel * fabsf(key);
+        want = want || (key >= lo - pad && key <= hi + pad);
+      }
+      want = want || (z_open && mine && !ex);
+      open = __syncthreads_or(want);
+    }
+    if (!open) break;
+    if (want) b.list[atomicAdd(&n_list, 1)] = (uint16_t)e;
+    __syncthreads();
+    fetch(n_list);
+    if (want) b.exact_f[e] = 1;
+  }
+  // slots: load, and the gates by warp 0 (every logit in float64)
+  for (int k = e; k < K; k += blockDim.x) {
+    const int id = b.top_id[k];
+    idx[k] = id;
+    atomicAdd(&counts[id], 1);
+  }
+  if (e >= 32) return;
+  const auto slot_x = [&](int k) { return b.x[b.top_id[k]]; };
+  double xm = -INFINITY, sm = 1.0, sum = 1.0;
+  bool ratio = false;
+  if (r.renorm) {
+    for (int k = lane; k < K; k += 32) {
+      const double v = slot_x(k);
+      xm = v > xm || v != v ? v : xm;
     }
     xm = sel_warp_max(xm);
-    const bool ratio = !softmax && !(xm < X(-30));
-    const X sm = ratio ? sel_sigmoid(xm) : X(1);
-    const auto weight = [&](int k) {
-      const X xk = slot_x(k);
-      return ratio ? sel_sigmoid(xk) / sm : sel_exp(xk - xm);
-    };
-    X sum = X(0);
-    for (int k = lane; k < r.K; k += 32) sum += weight(k);
+    ratio = !softmax && !(xm < -30.0);
+    if (ratio) sm = sel_sigmoid(xm);
+    sum = 0.0;
+    for (int k = lane; k < K; k += 32)
+      sum += ratio ? sel_sigmoid(slot_x(k)) / sm : exp(slot_x(k) - xm);
     sum = sel_warp_sum(sum);
-    for (int k = lane; k < r.K; k += 32) gate[k] = (float)(weight(k) / sum * (X)r.scale);
+  } else if (softmax) {
+    xm = m;
+    sum = z;
+  } else {
+    ratio = true;
   }
-  CloseCall out;
-  out.close = false;
-  out.mask = 0u;
-  if (!kExact) {
-    // the K-th against the next
-    uint32_t lb = 0u;
-#pragma unroll
-    for (int j = 0; j < V; ++j) lb = max(lb, ko[j]);
-    const uint32_t mx = __reduce_max_sync(0xffffffffu, lb);
-    if (mx) {
-      const float v = mx == 0xffffffffu ? NAN : sel_val(mx);
-      if (prev - v < 2.f * err + rel * (fabsf(prev) + fabsf(v))) {
-        lo = fminf(lo, v);
-        hi = fmaxf(hi, prev);
-      }
-    }
-    out.close = group_close || lo <= hi;
-    if (out.close) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int e = j * 32 + lane;
-        if (e >= N) continue;
-        // an expert whose key lies further than its bound from every close
-        // decision cannot take part in it; a softmax score needs every logit
-        const float pad = 3.f * err + 2.f * rel * fabsf(key[j]);
-        if (softmax || group_close || (key[j] >= lo - pad && key[j] <= hi + pad))
-          out.mask |= 1u << j;
-      }
-    }
+  for (int k = lane; k < K; k += 32) {
+    const double v = slot_x(k);
+    gate[k] = (float)((ratio ? sel_sigmoid(v) / sm : exp(v - xm)) / sum * (double)r.scale);
   }
-  return out;
 }
 
 }  // namespace moe
