@@ -252,6 +252,19 @@ moe_status launch_route_scored_backward(const void* u, const void* E, moe_dtype 
                                         const void* du_base, float* d_logit, void* du, float* dE,
                                         void* ws, cudaStream_t s);
 
+// router_grad_tc.cu ------------------------------------------------------------
+// bf16 planes hi, mid, lo of d_logit: [3][Tp][Np], zero rows from T, zero columns from N_r.
+struct RouterPlanes {
+  int Tp, Np;
+  size_t bytes;
+};
+RouterPlanes router_planes(int T, int N_r);
+size_t router_grad_tc_ws_bytes(int T, int d, int N_r);
+// du = du_base + d_logit E and dE = d_logit^T u, d_logit from the planes at the start of ws.
+moe_status launch_router_grad_tc(const void* u, const void* E, int T, int d, int N_r,
+                                 const void* du_base, void* du, float* dE, void* ws,
+                                 cudaStream_t s);
+
 // ep.cu ----------------------------------------------------------------------
 // Expert-parallel receive layout, dispatch and return (see ep.cu's header).
 moe_status launch_ep_plan(const int32_t* counts_all, int W, int rank, int N_r,

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(256) balance_final_kernel(
 }
 
 // ---------------------------------------------------------------- logit gradient
-// A warp per token.
+// A warp per token.  planes: d_logit as bf16 planes too (router_grad_tc.cu).
 constexpr int kGradWarps = 4;
 
 template <int V>
@@ -177,8 +177,16 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_logit_grad_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ idx,
     const float* __restrict__ d_gate, const int32_t* __restrict__ off, int n_seq,
     const float* __restrict__ coef, const float* __restrict__ d_loss, int T, int N, int K,
-    int softmax, int renorm, float scale, float* __restrict__ d_logit) {
+    int softmax, int renorm, float scale, float* __restrict__ d_logit,
+    __nv_bfloat16* __restrict__ planes, int Tp, int Np) {
   extern __shared__ float sm[];
+  // the planes' rows past the last token
+  if (planes) {
+    const long long pad = (long long)(Tp - T) * Np;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < 3 * pad;
+         i += (long long)gridDim.x * blockDim.x)
+      planes[((i / pad) * Tp + T) * (long long)Np + i % pad] = __float2bfloat16_rn(0.f);
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* row = sm + (size_t)warp * N;          // the token's scores, then its slots' terms
   for (int t = blockIdx.x * kGradWarps + warp; t < T; t += gridDim.x * kGradWarps) {
@@ -309,21 +317,36 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_logit_grad_kernel(
       const int e = j * 32 + lane;
       if (e < N) {
         const float dense = softmax ? s[j] * (q[j] - Q - R) : s[j] * om[j] * (q[j] - Q) * inv;
-        d_logit[(size_t)t * N + e] = dense + add[j];
+        add[j] += dense;
+        if (d_logit) d_logit[(size_t)t * N + e] = add[j];
+      } else {
+        add[j] = 0.f;
+      }
+      if (planes && e < Np) {
+        // hi + mid + lo: 24 bits in three roundings; an infinity stays in hi
+        const __nv_bfloat16 hi = __float2bfloat16_rn(add[j]);
+        const float fh = __bfloat162float(hi);
+        const float r1 = fabsf(fh) < INFINITY ? add[j] - fh : 0.f;
+        const __nv_bfloat16 mid = __float2bfloat16_rn(r1);
+        const __nv_bfloat16 lo = __float2bfloat16_rn(r1 - __bfloat162float(mid));
+        const size_t at = (size_t)t * Np + e, plane = (size_t)Tp * Np;
+        planes[at] = hi;
+        planes[at + plane] = mid;
+        planes[at + 2 * plane] = lo;
       }
     }
   }
 }
 
-// ---------------------------------------------------------------- CUDA-core products
+// ---------------------------------------------------------------- CUDA-core products (float32 u, E)
 // C[m, n] = base[m, n] + sum_k A(m, k) B[k, n], A(m, k) = A[m*lda + k] (or
 // A[k*lda + m] with TA) float32, B row-major.  64 x 64 tile per block, 4 x 4
 // outputs a thread, 16 steps of k staged at a time; every 256 steps the
 // running sums join a second set, so that a long sum keeps its low bits.
-template <typename TB, typename TC, bool TA>
+template <bool TA>
 __global__ void __launch_bounds__(256) router_product_kernel(
-    const float* __restrict__ A, int lda, const TB* __restrict__ B, int ldb,
-    const TC* __restrict__ base, TC* __restrict__ C, int M, int N, int Kd) {
+    const float* __restrict__ A, int lda, const float* __restrict__ B, int ldb,
+    const float* base, float* C, int M, int N, int Kd) {
   __shared__ float sa[16][64 + 4], sb[16][64 + 4];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
@@ -336,7 +359,7 @@ __global__ void __launch_bounds__(256) router_product_kernel(
       sa[k][m] = ok ? (TA ? A[(size_t)(k0 + k) * lda + m0 + m] : A[(size_t)(m0 + m) * lda + k0 + k])
                     : 0.f;
       const int kb = i >> 6, n = i & 63;
-      sb[kb][n] = k0 + kb < Kd && n0 + n < N ? IO<TB>::ld(B + (size_t)(k0 + kb) * ldb + n0 + n) : 0.f;
+      sb[kb][n] = k0 + kb < Kd && n0 + n < N ? B[(size_t)(k0 + kb) * ldb + n0 + n] : 0.f;
     }
     __syncthreads();
 #pragma unroll
@@ -364,7 +387,7 @@ __global__ void __launch_bounds__(256) router_product_kernel(
       const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
       if (m < M && n < N) {
         const size_t at = (size_t)m * N + n;
-        C[at] = IO<TC>::to(tot[i][j] + (base ? IO<TC>::cvt(base[at]) : 0.f));
+        C[at] = tot[i][j] + (base ? base[at] : 0.f);
       }
     }
 }
@@ -411,9 +434,8 @@ moe_status launch_balance_loss(const float* logits, const int32_t* idx, const in
 }
 
 size_t route_scored_bwd_ws_bytes(moe_dtype dt, int T, int d, int N_r) {
-  (void)dt;
-  (void)d;
-  return align_up((size_t)T * N_r * 4, 256);
+  // bf16: d_logit as bf16 planes and dE's slices; float32: d_logit itself
+  return dt == MOE_BF16 ? router_grad_tc_ws_bytes(T, d, N_r) : align_up((size_t)T * N_r * 4, 256);
 }
 
 moe_status launch_route_scored_backward(const void* u, const void* E, moe_dtype dt,
@@ -423,14 +445,18 @@ moe_status launch_route_scored_backward(const void* u, const void* E, moe_dtype 
                                         int N_r, int K, int score, int renorm, float scale,
                                         const void* du_base, float* d_logit, void* du, float* dE,
                                         void* ws, cudaStream_t s) {
-  float* dl = d_logit ? d_logit : static_cast<float*>(ws);
+  const bool tc = dt == MOE_BF16;
+  float* dl = d_logit || tc ? d_logit : static_cast<float*>(ws);
+  const RouterPlanes pl = router_planes(T, N_r);
+  __nv_bfloat16* planes = tc ? static_cast<__nv_bfloat16*>(ws) : nullptr;
   int blocks = (T + kGradWarps - 1) / kGradWarps;
   const size_t smem = (size_t)kGradWarps * N_r * 4;
   const int softmax = score == MOE_SCORE_SOFTMAX;
 #define MOE_GRAD(v)                                                                           \
   case v:                                                                                     \
     router_logit_grad_kernel<v><<<blocks, 32 * kGradWarps, smem, s>>>(                        \
-        logits, idx, d_gate, off, n_seq, coef, d_loss, T, N_r, K, softmax, renorm, scale, dl); \
+        logits, idx, d_gate, off, n_seq, coef, d_loss, T, N_r, K, softmax, renorm, scale, dl,  \
+        planes, pl.Tp, pl.Np);                                                                \
     break;
   switch (dispatch_v(N_r)) {
     MOE_GRAD(1) MOE_GRAD(2) MOE_GRAD(4) MOE_GRAD(8) MOE_GRAD(16) MOE_GRAD(32)
@@ -438,21 +464,13 @@ moe_status launch_route_scored_backward(const void* u, const void* E, moe_dtype 
 #undef MOE_GRAD
   moe_status st = cuda_check(cudaGetLastError(), "router_logit_grad launch");
   if (st != MOE_OK) return st;
+  if (tc) return launch_router_grad_tc(u, E, T, d, N_r, du_base, du, dE, ws, s);
   const dim3 gu((d + 63) / 64, (T + 63) / 64), ge((d + 63) / 64, (N_r + 63) / 64);
-  if (dt == MOE_F32) {
-    router_product_kernel<float, float, false><<<gu, 256, 0, s>>>(
-        dl, N_r, static_cast<const float*>(E), d, static_cast<const float*>(du_base),
-        static_cast<float*>(du), T, d, N_r);
-    router_product_kernel<float, float, true><<<ge, 256, 0, s>>>(
-        dl, N_r, static_cast<const float*>(u), d, nullptr, dE, N_r, d, T);
-  } else {
-    using bf = __nv_bfloat16;
-    router_product_kernel<bf, bf, false><<<gu, 256, 0, s>>>(
-        dl, N_r, static_cast<const bf*>(E), d, static_cast<const bf*>(du_base),
-        static_cast<bf*>(du), T, d, N_r);
-    router_product_kernel<bf, float, true><<<ge, 256, 0, s>>>(
-        dl, N_r, static_cast<const bf*>(u), d, nullptr, dE, N_r, d, T);
-  }
+  router_product_kernel<false><<<gu, 256, 0, s>>>(dl, N_r, static_cast<const float*>(E), d,
+                                                  static_cast<const float*>(du_base),
+                                                  static_cast<float*>(du), T, d, N_r);
+  router_product_kernel<true><<<ge, 256, 0, s>>>(dl, N_r, static_cast<const float*>(u), d, nullptr,
+                                                 dE, N_r, d, T);
   return cuda_check(cudaGetLastError(), "router_product launch");
 }
 
