@@ -31,12 +31,13 @@ constexpr int kPieces = 4;                   // 16-column pieces per epilogue wa
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kPairs = 74;                   // CTA pairs of 148 SMs
 
-// Barriers: full, empty per stage, tfull[2], tempty[2], mma_done, afull, aempty.
+// Barriers: full, empty per stage, tfull[2], tempty[2], mma_done, afull, aempty,
+// one for each epilogue warp's patch.
 template <int STAGES, int STAGE_BYTES, int FIXED_BYTES>
 struct Layout {
   static constexpr int OFF_FIXED = STAGES * STAGE_BYTES;
   static constexpr int OFF_BAR = OFF_FIXED + FIXED_BYTES;
-  static constexpr int N_BARS = 2 * STAGES + 7;
+  static constexpr int N_BARS = 2 * STAGES + 7 + kEpiWarps;
   static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
   static constexpr int ALLOC = OFF_MISC + 16 + 1024;
 };
@@ -46,35 +47,23 @@ __device__ __forceinline__ void raise_abort(volatile int* abort, int* err) {
   atomicOr(err, ERR_GEMM_TIMEOUT);
 }
 
-// 32 bytes of global memory: one access where the row is 32-byte aligned,
-// whole sectors either way.
-__device__ __forceinline__ void ld32(const void* p, bool wide, uint32_t (&r)[8]) {
-  if (wide) {
-    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7])
-                 : "l"(p)
-                 : "memory");
-  } else {
-    const uint4 a = static_cast<const uint4*>(p)[0], b = static_cast<const uint4*>(p)[1];
-    r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
-    r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
-  }
-}
-__device__ __forceinline__ void st32(void* p, bool wide, const uint32_t (&r)[8]) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-  } else {
-    static_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-    static_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
-  }
+// 32 bytes (a whole sector) in one store; p is 32-byte aligned.
+__device__ __forceinline__ void st32(void* p, const float* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p),
+               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+               : "memory");
 }
 
 // ---------------------------------------------------------------- dE
-// A pair owns 256 experts (128 rows of C per CTA) x a slab of 256 columns x
-// one of S slices of the tokens.  Both operands are MN-major (the contraction
+// A tile is 256 experts (128 rows of C per CTA of a pair) x a slab of 256
+// columns; its work is one unit for each 64 tokens.  The units of all tiles,
+// in order, are dealt to the pairs in equal runs, so every pair is busy to the
+// end whatever the number of tiles; a run's part of a tile is a segment, kept
+// as a float32 [256][256] block numbered pair + tile (either number grows
+// along the units, so the blocks are distinct), and router_de_join_kernel adds
+// a tile's segments in order.  Both operands are MN-major (the contraction
 // runs over token rows): per stage of 64 tokens each CTA holds its 128 experts
 // of the three planes (48 KB) and its half of the slab of u (16 KB); u is
 // loaded once for the three planes.  36 accumulation steps (three stages) go
@@ -88,11 +77,15 @@ using ELay = Layout<E_STAGES, E_A + E_B, 0>;
 struct DeParams {
   int T, Tp, N_r, d;
   int nk;                    // Tp / 64
-  int n_et, n_slab, S;
-  float* C;                  // [S][N_r][d]
-  bool wide;
+  int n_et, n_slab, n_pairs;
+  float* C;                  // segments [n_pairs + tiles][256][256]
   int* err;
 };
+
+// First unit of pair c of P over U units.
+__host__ __device__ __forceinline__ int first_unit(int c, int P, int U) {
+  return (int)((long long)c * U / P);
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     router_de_kernel(const __grid_constant__ CUtensorMap tmD,
@@ -130,19 +123,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t full0 = map_shared_to(smem_u32(&full[0]), 0);
   const uint32_t tempty0 = map_shared_to(smem_u32(&tempty[0]), 0);
-  const int items = p.n_et * p.n_slab * p.S, step = (int)n_clusters_x();
-  const int first = (int)cluster_id_x();
+  const int pair = (int)cluster_id_x(), units = p.n_et * p.n_slab * p.nk;
+  const int u0 = first_unit(pair, p.n_pairs, units), u1 = first_unit(pair + 1, p.n_pairs, units);
 
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int it = first; it < items && ok; it += step) {
-        const int slab = it % p.n_slab, sl = (it / p.n_slab) % p.S, et = it / p.n_slab / p.S;
+      for (int un = u0; un < u1 && ok;) {
+        const int tile = un / p.nk, slab = tile % p.n_slab, et = tile / p.n_slab;
         const int e0 = et * 256 + (int)half * 128, c0 = slab * BN + (int)half * 128;
-        const int k1 = (int)((long long)(sl + 1) * p.nk / p.S);
-        for (int kb = (int)((long long)sl * p.nk / p.S); kb < k1; ++kb) {
+        const int end = min(u1, (tile + 1) * p.nk);
+        for (; un < end; ++un) {
+          const int kb = un - tile * p.nk;
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitNs)) {
             raise_abort(abort_flag, p.err);
             ok = false;
@@ -173,11 +167,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, buf = 0;
       uint32_t phase = 0, tphase = 0;
       bool ok = true;
-      for (int it = first; it < items && ok; it += step) {
-        const int sl = (it / p.n_slab) % p.S;
-        const int k0 = (int)((long long)sl * p.nk / p.S);
-        const int k1 = (int)((long long)(sl + 1) * p.nk / p.S);
-        for (int c0 = k0; c0 < k1 && ok; c0 += E_CHUNK) {
+      for (int un = u0; un < u1 && ok;) {
+        const int k1 = min(u1, (un / p.nk + 1) * p.nk);      // the segment's end
+        for (int c0 = un; c0 < k1 && ok; c0 += E_CHUNK) {
           if (!mbar_wait_bounded(&tempty[buf], tphase ^ 1, abort_flag, kWaitNs)) {
             raise_abort(abort_flag, p.err);
             ok = false;
@@ -208,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma2_commit_mask(&tfull[buf], 3);
           if (++buf == 2) { buf = 0; tphase ^= 1; }
         }
+        un = k1;
       }
       mma2_commit_local(mma_done);
       mbar_wait_bounded(mma_done, 0, nullptr, kWaitNs);
@@ -218,10 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int buf = 0;
     uint32_t tphase = 0;
     bool ok = true;
-    for (int it = first; it < items && ok; it += step) {
-      const int slab = it % p.n_slab, sl = (it / p.n_slab) % p.S, et = it / p.n_slab / p.S;
-      const int k0 = (int)((long long)sl * p.nk / p.S);
-      const int k1 = (int)((long long)(sl + 1) * p.nk / p.S);
+    for (int un = u0; un < u1 && ok;) {
+      const int tile = un / p.nk, k0 = un, k1 = min(u1, (tile + 1) * p.nk);
       float acc[kPieces][16];
 #pragma unroll
       for (int i = 0; i < kPieces; ++i)
@@ -249,23 +240,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++buf == 2) { buf = 0; tphase ^= 1; }
       }
       if (!ok) break;
-      const int e = et * 256 + (int)half * 128 + q * 32 + lane;
-      if (e < p.N_r) {
-        float* out = p.C + ((size_t)sl * p.N_r + e) * p.d;
+      // experts past N_r are zero rows: not kept
+      const int row = (int)half * 128 + q * 32 + lane;
+      if (tile / p.n_slab * 256 + row < p.N_r) {
+        float* out = p.C + ((size_t)(pair + tile) * 256 + row) * BN + part * 64;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          const int c = slab * BN + part * 64 + i * 16;
-          if (c < p.d) {
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              uint32_t w[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(acc[i][8 * v + j]);
-              st32(out + c + 8 * v, p.wide, w);
-            }
-          }
+          st32(out + i * 16, &acc[i][0]);
+          st32(out + i * 16 + 8, &acc[i][8]);
         }
       }
+      un = k1;
     }
   }
   tc_fence_before();
@@ -277,18 +262,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// dE = sum of its S slices, in slice order.
-__global__ void __launch_bounds__(256) router_de_join_kernel(const float4* __restrict__ P, int S,
-                                                             long long n4,
-                                                             float4* __restrict__ dE) {
-  const long long step = (long long)gridDim.x * blockDim.x;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n4; i += step) {
-    float4 a = P[i];
-    for (int s = 1; s < S; ++s) {
-      const float4 b = P[i + s * n4];
+// Adds a tile's segments in order: a block per tile and kJoinRows of its rows,
+// a float4 of 64 columns-of-four per thread.
+constexpr int kJoinRows = 8;
+__global__ void __launch_bounds__(256) router_de_join_kernel(const float* __restrict__ C, int P,
+                                                             int nk, int n_slab, int units,
+                                                             int N_r, int d,
+                                                             float* __restrict__ dE) {
+  __shared__ int s_c0, s_c1;
+  const int tile = blockIdx.x, slab = tile % n_slab, e0 = tile / n_slab * 256;
+  if (threadIdx.x == 0) {
+    // the pairs whose runs meet the tile's units
+    int c0 = (int)((long long)tile * nk * P / units);
+    while (c0 > 0 && first_unit(c0, P, units) > tile * nk) --c0;
+    while (first_unit(c0 + 1, P, units) <= tile * nk) ++c0;
+    int c1 = c0 + 1;
+    while (c1 < P && first_unit(c1, P, units) < (tile + 1) * nk) ++c1;
+    s_c0 = c0;
+    s_c1 = c1;
+  }
+  __syncthreads();
+  const int c0 = s_c0, c1 = s_c1, c4 = (threadIdx.x & 63) * 4;
+#pragma unroll
+  for (int k = 0; k < kJoinRows / 4; ++k) {
+    const int row = blockIdx.y * kJoinRows + k * 4 + (threadIdx.x >> 6);
+    if (e0 + row >= N_r || slab * BN + c4 >= d) continue;
+    const float* src = C + ((size_t)(c0 + tile) * 256 + row) * BN + c4;
+    float4 a = *reinterpret_cast<const float4*>(src);
+#pragma unroll 4
+    for (int c = c0 + 1; c < c1; ++c) {
+      src += 256 * BN;
+      const float4 b = *reinterpret_cast<const float4*>(src);
       a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
     }
-    dE[i] = a;
+    *reinterpret_cast<float4*>(dE + (size_t)(e0 + row) * d + slab * BN + c4) = a;
   }
 }
 
@@ -296,32 +303,44 @@ __global__ void __launch_bounds__(256) router_de_join_kernel(const float4* __res
 // A pair owns 256 tokens (128 per CTA) and a run of 256-column slabs.  The
 // token rows of both planes (K-major) stay in shared memory for the whole run
 // where N_r <= 256 (RES: 128 KB), so a slab streams only its half of E
-// (MN-major, 16 KB per 64 experts); otherwise each stage brings both planes'
-// rows again.  Two TMEM buffers: the epilogue of a slab (base rows read ahead,
-// added in float32, rounded once) runs under the next slab's products.  Bound
-// by reading du_base and writing du.
-constexpr int U_A = 2 * 128 * BK * 2, U_B = 2 * kBox;       // 32 KB, 16 KB
+// (MN-major, 8 KB per 32 experts); otherwise each stage brings both planes'
+// rows again (64 experts).  Two TMEM buffers: the epilogue of a slab runs under the next
+// slab's products.  Each epilogue warp owns a [32 tokens][64 columns] patch
+// (128-byte swizzle): TMA brings the base values, the warp adds its float32
+// sums, rounds once and writes them back in place, TMA takes them out; the
+// next slab's patch is fetched while its sums are being made.  At T 8192, d
+// 7168, N_r 256 this takes 71 us (61 without a base): what holds it back is the
+// pair's round trip for a stage of E (commit, both producers, L2, the leader's
+// barrier: some 3600 cycles against the 2048 tensor cycles in the ring).
+// Measured instead: a ring twice as large leaves room for patches of 2 KB
+// only, 52 us without a base but 80 with one; row accesses straight from the
+// lanes touch 32 lines an instruction, 82 us.
+constexpr int U_A = 2 * 128 * BK * 2;                       // both planes' rows of 64 experts
 constexpr int U_RES_BLOCKS = 4;                             // 4 x 64 experts resident
 template <bool RES>
-struct ULay : Layout<4, RES ? U_B : U_A + U_B, RES ? U_RES_BLOCKS * U_A : 0> {
-  static constexpr int STAGES = 4;
-  static constexpr int STAGE_BYTES = RES ? U_B : U_A + U_B;
+struct ULay : Layout<RES ? 4 : 3, RES ? kBox : U_A + 2 * kBox,
+                     (RES ? U_RES_BLOCKS * U_A : 0) + kEpiWarps * 4096> {
+  static constexpr int STAGES = RES ? 4 : 3;
+  static constexpr int KB = RES ? 32 : 64;                  // experts per stage
+  static constexpr int B_BOX = KB * 128;                    // [KB][64 columns]
+  static constexpr int STAGE_BYTES = RES ? kBox : U_A + 2 * kBox;
+  static constexpr int OFF_PATCH = ULay::OFF_FIXED + (RES ? U_RES_BLOCKS * U_A : 0);
 };
 
 struct DuParams {
   int T, Tp, d;
-  int nk;                    // ceil(Np / 64)
+  int nk, n_stage;           // blocks of 64 experts; stages of L::KB experts
   int n_tt, n_slab, n_run;   // token tiles, slabs, runs of slabs per token tile
-  const __nv_bfloat16* base; // or nullptr
-  __nv_bfloat16* du;
-  bool wide_in, wide_out;
+  bool base;                 // tmBase is read
   int* err;
 };
 
 template <bool RES>
 __global__ void __launch_bounds__(kThreads, 1)
     router_du_kernel(const __grid_constant__ CUtensorMap tmD,
-                     const __grid_constant__ CUtensorMap tmE, const DuParams p) {
+                     const __grid_constant__ CUtensorMap tmE,
+                     const __grid_constant__ CUtensorMap tmBase,
+                     const __grid_constant__ CUtensorMap tmOut, const DuParams p) {
   using L = ULay<RES>;
   constexpr int STAGES = L::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -334,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* mma_done = tempty + 2;
   uint64_t* afull = mma_done + 1;
   uint64_t* aempty = afull + 1;
+  uint64_t* pbar = aempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -346,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(mma_done, 1);
     mbar_init(afull, 1);
     mbar_init(aempty, 1);
+    for (int w = 0; w < kEpiWarps; ++w) mbar_init(&pbar[w], 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmD);
@@ -388,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s1 = (int)((long long)(run + 1) * p.n_slab / p.n_run);
         for (int slab = (int)((long long)run * p.n_slab / p.n_run); slab < s1 && ok; ++slab) {
           const int c0 = slab * BN + (int)half * 128;
-          for (int kb = 0; kb < p.nk; ++kb) {
+          for (int kb = 0; kb < p.n_stage; ++kb) {
             if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitNs)) {
               raise_abort(abort_flag, p.err);
               ok = false;
@@ -399,10 +420,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* b = smem + stage * L::STAGE_BYTES;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              tma_load_2d_pair(b + j * kBox, &tmE, c0 + 64 * j, kb * BK, fb);
+              tma_load_2d_pair(b + j * L::B_BOX, &tmE, c0 + 64 * j, kb * L::KB, fb);
             if (!RES)
               for (int pl = 0; pl < 2; ++pl)
-                tma_load_2d_pair(b + U_B + pl * (U_A / 2), &tmD, kb * BK, pl * p.Tp + t0, fb);
+                tma_load_2d_pair(b + 2 * L::B_BOX + pl * (U_A / 2), &tmD, kb * L::KB,
+                                 pl * p.Tp + t0, fb);
             if (++stage == STAGES) { stage = 0; phase ^= 1; }
           }
         }
@@ -434,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          for (int kb = 0; kb < p.nk; ++kb) {
+          for (int kb = 0; kb < p.n_stage; ++kb) {
             if (!mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitNs)) {
               raise_abort(abort_flag, p.err);
               ok = false;
@@ -442,13 +464,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const uint32_t b0 = smem_u32(smem + stage * L::STAGE_BYTES);
-            const uint32_t a0 = RES ? smem_u32(smem + L::OFF_FIXED + kb * U_A) : b0 + U_B;
+            // RES: the second stage of a 64-expert block starts 64 bytes into its rows
+            const uint32_t a0 = RES ? smem_u32(smem + L::OFF_FIXED + (kb >> 1) * U_A) + (kb & 1) * 64
+                                    : b0 + 2 * L::B_BOX;
 #pragma unroll
             for (int pl = 1; pl >= 0; --pl)
 #pragma unroll
-              for (int k = 0; k < BK / 16; ++k)
+              for (int k = 0; k < L::KB / 16; ++k)
                 mma2_f16_ss(tmem_base + buf * BN, smem_desc_k_sw128(a0 + pl * (U_A / 2) + k * 32),
-                            smem_desc_mn_sw128(b0 + k * 2048, kBox), idesc,
+                            smem_desc_mn_sw128(b0 + k * 2048, L::B_BOX), idesc,
                             (kb > 0 || pl < 1 || k > 0) ? 1u : 0u);
             mma2_commit_mask(&empty[stage], 3);
             if (++stage == STAGES) { stage = 0; phase ^= 1; }
@@ -465,28 +489,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     const int q = warp & 3, part = (warp - 2) >> 2;
     const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    uint4* patch = reinterpret_cast<uint4*>(smem + L::OFF_PATCH + (warp - 2) * 4096);   // [32][8]
+    uint64_t* pb = &pbar[warp - 2];
     int buf = 0;
-    uint32_t tphase = 0;
-    bool ok = true;
+    uint32_t tphase = 0, pphase = 0;
+    bool ok = true, armed = false;
+    const auto row_of = [&](int it) { return it / p.n_run * 256 + (int)half * 128 + q * 32; };
+    const auto slab0 = [&](int it) { return (int)((long long)(it % p.n_run) * p.n_slab / p.n_run); };
+    const auto slab1 = [&](int it) { return (int)((long long)(it % p.n_run + 1) * p.n_slab / p.n_run); };
+    // d is a multiple of 64: a patch's columns are all inside or all outside
+    const auto live = [&](int it, int c) { return row_of(it) < p.T && c < p.d; };
+    // fetches a slab's base values (the store out of the patch has to have read it)
+    const auto fetch = [&](int it, int slab) {
+      const int c = slab * BN + part * 64;
+      if (!p.base || !live(it, c)) return;
+      if (lane == 0) {
+        tma_store_wait_read_all();
+        mbar_arrive_expect_tx(pb, 4096);
+        tma_load_2d(patch, &tmBase, c, row_of(it), pb);
+      }
+      armed = true;
+    };
+    if (first < items) fetch(first, slab0(first));
     for (int it = first; it < items && ok; it += step) {
-      const int tt = it / p.n_run, run = it % p.n_run;
-      const int t = tt * 256 + (int)half * 128 + q * 32 + lane;
-      const int s1 = (int)((long long)(run + 1) * p.n_slab / p.n_run);
-      for (int slab = (int)((long long)run * p.n_slab / p.n_run); slab < s1; ++slab) {
-        const int c0 = slab * BN + part * 64;
-        // d is a multiple of 64, so this warp's 64 columns are all inside or all outside
-        const bool live = t < p.T && c0 < p.d;
-        const size_t at = (size_t)t * p.d + c0;
-        uint32_t bs[kPieces][8];
-        if (live && p.base) {
-#pragma unroll
-          for (int i = 0; i < kPieces; ++i) ld32(p.base + at + i * 16, p.wide_in, bs[i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) bs[i][j] = 0u;
-        }
+      const int s1 = slab1(it);
+      for (int slab = slab0(it); slab < s1; ++slab) {
         const bool got = mbar_wait_bounded(&tfull[buf], tphase, abort_flag, kWaitNs);
         if (!__all_sync(0xffffffffu, got)) {
           if (lane == 0) raise_abort(abort_flag, p.err);
@@ -494,29 +521,53 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          uint32_t r[16];
-          tmem_ld_32x32b_x16(trow + buf * BN + part * 64 + i * 16, r);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float lo = __uint_as_float(bs[i][j] << 16) + __uint_as_float(r[2 * j]);
-            const float hi = __uint_as_float(bs[i][j] & 0xffff0000u) + __uint_as_float(r[2 * j + 1]);
-            const __nv_bfloat162 w = __floats2bfloat162_rn(lo, hi);
-            bs[i][j] = *reinterpret_cast<const uint32_t*>(&w);
-          }
-        }
+        uint32_t r[2][32];
+        tmem_ld_32x32b_x32(trow + buf * BN + part * 64, r[0]);
+        tmem_ld_32x32b_x32(trow + buf * BN + part * 64 + 32, r[1]);
+        tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(tempty0 + buf * 8);
         if (++buf == 2) { buf = 0; tphase ^= 1; }
-        if (live) {
+        const int c = slab * BN + part * 64;
+        if (live(it, c)) {
+          if (p.base) {
+            const bool in = mbar_wait_bounded(pb, pphase, abort_flag, kWaitNs);
+            if (!__all_sync(0xffffffffu, in)) {
+              if (lane == 0) raise_abort(abort_flag, p.err);
+              ok = false;
+              break;
+            }
+            pphase ^= 1;
+            armed = false;
+          } else {
+            if (lane == 0) tma_store_wait_read_all();
+            __syncwarp();
+          }
+          // row `lane`: 16-byte slot i sits at i ^ (row & 7)
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) st32(p.du + at + i * 16, p.wide_out, bs[i]);
+          for (int i = 0; i < 8; ++i) {
+            uint4* at = patch + lane * 8 + (i ^ (lane & 7));
+            float f[8];
+            Vec<__nv_bfloat16>::load(p.base ? *at : make_uint4(0u, 0u, 0u, 0u), f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] += __uint_as_float(r[i >> 2][8 * (i & 3) + j]);
+            *at = Vec<__nv_bfloat16>::store(f);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmOut, patch, c, row_of(it));
+            tma_store_commit();
+          }
         }
+        if (slab + 1 < s1) fetch(it, slab + 1);
+        else if (it + step < items) fetch(it + step, slab0(it + step));
       }
     }
+    // no copy may still use shared memory when the CTA leaves
+    if (armed) mbar_wait_bounded(pb, pphase, nullptr, kWaitNs);
+    if (lane == 0) tma_store_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -527,15 +578,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename Kern, typename Params>
-moe_status launch_pairs(Kern kern, const CUtensorMap& a, const CUtensorMap& b, const Params& p,
-                        long long items, int smem, bool* attr_done, const char* what,
-                        cudaStream_t s) {
+template <typename... Params, typename... Args>
+moe_status launch_pairs(void (*kern)(Params...), long long pairs, int smem, bool* attr_done,
+                        const char* what, cudaStream_t s, const Args&... args) {
   const moe_status st = ensure_max_smem(reinterpret_cast<const void*>(kern), smem, attr_done, what);
   if (st != MOE_OK) return st;
-  const int pairs = sm_count() / 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * (unsigned)(items < pairs ? items : pairs));
+  cfg.gridDim = dim3(2 * (unsigned)pairs);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -546,24 +595,20 @@ moe_status launch_pairs(Kern kern, const CUtensorMap& a, const CUtensorMap& b, c
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, kern, a, b, p), what);
+  return cuda_check(cudaLaunchKernelEx(&cfg, kern, args...), what);
 }
 
-bool al32(const void* p) { return reinterpret_cast<uintptr_t>(p) % 32 == 0; }
-
-// Slices of the tokens for dE: as many as fill the GPU's pairs once, each of
-// at least two stages.
-int de_slices(int T, int d, int N_r) {
-  const int items = (N_r + 255) / 256 * ((d + BN - 1) / BN), nk = (T + BK - 1) / BK;
-  int S = kPairs / items;
-  if (S > nk / 2) S = nk / 2;
-  if (S > 16) S = 16;
-  return S < 1 ? 1 : S;
+// Pairs that share dE's units: all of the GPU's, but none with fewer than two.
+int de_pairs(int T, int d, int N_r) {
+  const long long units = (long long)((N_r + 255) / 256) * ((d + BN - 1) / BN) *
+                          ((T + BK - 1) / BK);
+  const long long most = units < 2 ? 1 : units / 2;
+  return (int)(most < kPairs ? most : kPairs);
 }
 
 }  // namespace
 
-// Planes [3][Tp][Np], then the slices of dE where there is more than one.
+// Planes [3][Tp][Np], then the segments of dE.
 RouterPlanes router_planes(int T, int N_r) {
   RouterPlanes r;
   r.Tp = (T + BK - 1) / BK * BK;
@@ -573,8 +618,8 @@ RouterPlanes router_planes(int T, int N_r) {
 }
 
 size_t router_grad_tc_ws_bytes(int T, int d, int N_r) {
-  const int S = de_slices(T, d, N_r);
-  return router_planes(T, N_r).bytes + (S > 1 ? align_up((size_t)S * N_r * d * 4, 256) : 0);
+  const size_t tiles = (size_t)((N_r + 255) / 256) * ((d + BN - 1) / BN);
+  return router_planes(T, N_r).bytes + (de_pairs(T, d, N_r) + tiles) * 256 * BN * 4;
 }
 
 moe_status launch_router_grad_tc(const void* u, const void* E, int T, int d, int N_r,
@@ -584,7 +629,7 @@ moe_status launch_router_grad_tc(const void* u, const void* E, int T, int d, int
   int* err = device_error_word();
   if (!err) return fail(MOE_ERR_CUDA, "device error word unavailable");
   const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  CUtensorMap tmA, tmB;
+  CUtensorMap tmA, tmB, tmBase, tmOut;
   moe_status st;
   {
     DuParams p;
@@ -592,28 +637,29 @@ moe_status launch_router_grad_tc(const void* u, const void* E, int T, int d, int
     p.Tp = pl.Tp;
     p.d = d;
     p.nk = (pl.Np + BK - 1) / BK;
+    const bool res = p.nk <= U_RES_BLOCKS;
+    const int kb = res ? ULay<true>::KB : ULay<false>::KB;
+    p.n_stage = (pl.Np + kb - 1) / kb;
     p.n_tt = (T + 255) / 256;
     p.n_slab = (d + BN - 1) / BN;
     // runs of slabs per token tile: enough to give every pair one
     p.n_run = kPairs / p.n_tt;
     if (p.n_run > p.n_slab) p.n_run = p.n_slab;
     if (p.n_run < 1) p.n_run = 1;
-    p.base = static_cast<const __nv_bfloat16*>(du_base);
-    p.du = static_cast<__nv_bfloat16*>(du);
-    p.wide_in = al32(du_base);
-    p.wide_out = al32(du);
+    p.base = du_base != nullptr;
     p.err = err;
     st = make_tmap_2d(&tmA, ws, bf, 2, pl.Np, (uint64_t)3 * pl.Tp, BK, 128);
-    if (st != MOE_OK) return st;
-    st = make_tmap_2d(&tmB, E, bf, 2, d, N_r, 64, BK);
+    if (st == MOE_OK) st = make_tmap_2d(&tmB, E, bf, 2, d, N_r, 64, kb);
+    if (st == MOE_OK) st = make_tmap_2d(&tmOut, du, bf, 2, d, T, 64, 32);
+    if (st == MOE_OK) st = make_tmap_2d(&tmBase, du_base ? du_base : du, bf, 2, d, T, 64, 32);
     if (st != MOE_OK) return st;
     static bool done_r[kMaxSmemDevices] = {}, done_s[kMaxSmemDevices] = {};
     const long long items = (long long)p.n_tt * p.n_run;
-    st = p.nk <= U_RES_BLOCKS
-             ? launch_pairs(router_du_kernel<true>, tmA, tmB, p, items, ULay<true>::ALLOC, done_r,
-                            "router_du launch", s)
-             : launch_pairs(router_du_kernel<false>, tmA, tmB, p, items, ULay<false>::ALLOC,
-                            done_s, "router_du launch", s);
+    const long long pairs = items < kPairs ? items : kPairs;
+    st = res ? launch_pairs(router_du_kernel<true>, pairs, ULay<true>::ALLOC, done_r,
+                            "router_du launch", s, tmA, tmB, tmBase, tmOut, p)
+             : launch_pairs(router_du_kernel<false>, pairs, ULay<false>::ALLOC, done_s,
+                            "router_du launch", s, tmA, tmB, tmBase, tmOut, p);
     if (st != MOE_OK) return st;
   }
   DeParams p;
@@ -624,24 +670,20 @@ moe_status launch_router_grad_tc(const void* u, const void* E, int T, int d, int
   p.nk = pl.Tp / BK;
   p.n_et = (N_r + 255) / 256;
   p.n_slab = (d + BN - 1) / BN;
-  p.S = de_slices(T, d, N_r);
-  float* part = p.S > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + pl.bytes) : dE;
-  p.C = part;
-  p.wide = al32(part);
+  p.n_pairs = de_pairs(T, d, N_r);
+  p.C = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + pl.bytes);
   p.err = err;
   st = make_tmap_2d(&tmA, ws, bf, 2, pl.Np, (uint64_t)3 * pl.Tp, 64, BK);
-  if (st != MOE_OK) return st;
-  st = make_tmap_2d(&tmB, u, bf, 2, d, T, 64, BK);
+  if (st == MOE_OK) st = make_tmap_2d(&tmB, u, bf, 2, d, T, 64, BK);
   if (st != MOE_OK) return st;
   static bool done_e[kMaxSmemDevices] = {};
-  st = launch_pairs(router_de_kernel, tmA, tmB, p, (long long)p.n_et * p.n_slab * p.S, ELay::ALLOC,
-                    done_e, "router_de launch", s);
-  if (st != MOE_OK || p.S == 1) return st;
-  const long long n4 = (long long)N_r * d / 4;
-  const long long blocks = (n4 + 255) / 256;
-  router_de_join_kernel<<<(unsigned)(blocks < 8 * sm_count() ? blocks : 8 * sm_count()), 256, 0,
-                          s>>>(reinterpret_cast<const float4*>(part), p.S, n4,
-                               reinterpret_cast<float4*>(dE));
+  st = launch_pairs(router_de_kernel, p.n_pairs, ELay::ALLOC, done_e, "router_de launch", s, tmA,
+                    tmB, p);
+  if (st != MOE_OK) return st;
+  const int rows = N_r < 256 ? N_r : 256;
+  const dim3 grid(p.n_et * p.n_slab, (rows + kJoinRows - 1) / kJoinRows);
+  router_de_join_kernel<<<grid, 256, 0, s>>>(p.C, p.n_pairs, p.nk, p.n_slab,
+                                            p.n_et * p.n_slab * p.nk, N_r, d, dE);
   return cuda_check(cudaGetLastError(), "router_de_join launch");
 }
 
