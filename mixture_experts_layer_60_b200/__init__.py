@@ -405,10 +405,15 @@ def _want(who, **tensors):
             raise ValueError(f"{who}: {name} has shape {tuple(t.shape)}, not {shape}")
 
 
-def _here(who, t):
-    """The library launches on the current device: its tensors have to live there."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
+def _here(who, t, stream):
+    """The stream's handle (None: the current one of the current device).  The library launches on
+    the current device: the call's tensors have to live there."""
+    if not t.is_cuda:
+        raise ValueError("libmoe takes device tensors only")
+    dev = torch._C._cuda_getDevice()
+    if t.get_device() != dev:
         raise ValueError(f"{who}: tensors are on {t.device}, not on the current device")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _s(stream)
 
 
 def moe_route_scored_workspace_size(T: int, d: int, N_r: int) -> int:
@@ -424,14 +429,14 @@ def moe_route_scored(u, E, b, K, topk_idx, topk_gate, counts, workspace,
     who = "moe_route_scored"
     T, d = u.shape
     N_r = E.shape[0]
-    _here(who, u)
+    st = _here(who, u, stream)
     _want(who, E=(E, u.dtype, (N_r, d)), b=(b, _F32, (N_r,)), topk_idx=(topk_idx, _I32, (T, K)),
           topk_gate=(topk_gate, _F32, (T, K)), counts=(counts, _I32, (N_r,)),
           logits=(logits, _F32, (T, N_r)))
     _check(lib().moe_route_scored(_p(u), _p(E), _dt(u), _p(b), T, d, N_r, K, score, n_groups,
                                   topk_groups, group_top, 1 if renorm else 0, gate_scale,
                                   _p(topk_idx), _p(topk_gate), _p(counts), _p(logits),
-                                  _p(workspace), _nbytes(workspace), _s(stream)))
+                                  _p(workspace), _nbytes(workspace), st))
 
 
 def moe_balance_loss_workspace_size(T: int, N_r: int, n_seq: int) -> int:
@@ -445,13 +450,13 @@ def moe_balance_loss(logits, topk_idx, alpha, loss, coef, workspace, score=MOE_S
     T, N_r = logits.shape
     n_seq = loss.shape[0]
     K = topk_idx.shape[1]
-    _here(who, logits)
+    st = _here(who, logits, stream)
     _want(who, logits=(logits, _F32, (T, N_r)), topk_idx=(topk_idx, _I32, (T, K)),
           loss=(loss, _F32, (n_seq,)), coef=(coef, _F32, (n_seq, N_r)),
           seq_offsets=(seq_offsets, _I32, (n_seq + 1,)))
     _check(lib().moe_balance_loss(_p(logits), _p(topk_idx), _p(seq_offsets), n_seq, T, N_r, K,
                                   score, alpha, _p(loss), _p(coef), _p(workspace),
-                                  _nbytes(workspace), _s(stream)))
+                                  _nbytes(workspace), st))
 
 
 def moe_route_scored_backward_workspace_size(dt: int, T: int, d: int, N_r: int) -> int:
@@ -470,7 +475,7 @@ def moe_route_scored_backward(u, E, logits, topk_idx, d_gate, du, dE, workspace,
     N_r = E.shape[0]
     K = topk_idx.shape[1]
     n_seq = 1 if balance_coef is None else balance_coef.shape[0]
-    _here(who, u)
+    st = _here(who, u, stream)
     _want(who, E=(E, u.dtype, (N_r, d)), logits=(logits, _F32, (T, N_r)),
           topk_idx=(topk_idx, _I32, (T, K)), d_gate=(d_gate, _F32, (T, K)),
           du=(du, u.dtype, (T, d)), dE=(dE, _F32, (N_r, d)), du_base=(du_base, u.dtype, (T, d)),
@@ -482,7 +487,7 @@ def moe_route_scored_backward(u, E, logits, topk_idx, d_gate, du, dE, workspace,
     _check(lib().moe_route_scored_backward(
         _p(u), _p(E), _dt(u), _p(logits), _p(topk_idx), _p(d_gate), _p(seq_offsets), n_seq,
         _p(balance_coef), _p(d_loss), T, d, N_r, K, score, 1 if renorm else 0, gate_scale,
-        _p(du_base), _p(d_logit), _p(du), _p(dE), _p(workspace), _nbytes(workspace), _s(stream)))
+        _p(du_base), _p(d_logit), _p(du), _p(dE), _p(workspace), _nbytes(workspace), st))
 
 
 # ------------------------------------------------------------------ 8-bit checkpoints
@@ -496,13 +501,13 @@ def moe_expert_gate_up_save8(x, offsets, W_gate_up, h, a_q, a_scale, stream=None
     who = "moe_expert_gate_up_save8"
     rows, d = x.shape
     n_groups, two_i, _ = W_gate_up.shape
-    _here(who, x)
+    st = _here(who, x, stream)
     _want(who, W_gate_up=(W_gate_up, x.dtype, (n_groups, two_i, d)),
           offsets=(offsets, _I32, (n_groups + 1,)), h=(h, x.dtype, (rows, two_i // 2)),
           a_q=(a_q, _E4M3, (rows, two_i)), a_scale=(a_scale, _F32, (rows, two_i // 128)))
     _check(lib().moe_expert_gate_up_save8(_p(x), _p(offsets), n_groups, rows, d, two_i // 2,
                                           _dt(x), _p(W_gate_up), _p(h), _p(a_q), _p(a_scale),
-                                          _s(stream)))
+                                          st))
 
 
 def moe_expert_ffn_backward8_workspace_size(dt: int, rows: int, d: int, I: int,
@@ -516,7 +521,7 @@ def moe_expert_ffn_backward8(x, offsets, W_gate_up, W_down, a_q, a_scale, dy, dx
     who = "moe_expert_ffn_backward8"
     rows, d = dy.shape
     n_groups, two_i, _ = W_gate_up.shape
-    _here(who, x)
+    st = _here(who, x, stream)
     t = x.dtype
     _want(who, x=(x, t, (rows, d)), W_gate_up=(W_gate_up, t, (n_groups, two_i, d)),
           W_down=(W_down, t, (n_groups, d, two_i // 2)), offsets=(offsets, _I32, (n_groups + 1,)),
@@ -527,7 +532,7 @@ def moe_expert_ffn_backward8(x, offsets, W_gate_up, W_down, a_q, a_scale, dy, dx
     _check(lib().moe_expert_ffn_backward8(
         _p(x), _p(offsets), n_groups, rows, d, two_i // 2, _dt(x), _p(W_gate_up), _p(W_down),
         _p(a_q), _p(a_scale), _p(dy), _p(dx), _p(dW_gate_up), _p(dW_down), _p(workspace),
-        _nbytes(workspace), _s(stream)))
+        _nbytes(workspace), st))
 
 
 # ------------------------------------------------------------------ expert parallelism

@@ -41,6 +41,28 @@ moe_status check_sm100();
 const char* last_error_text();
 void clear_last_error();
 
+// Launches a kernel that calls pdl_wait() so that it may overlap the tail of
+// the stream's previous kernel; cluster > 1: in clusters of that many blocks.
+template <typename... P, typename... A>
+moe_status launch_after(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                        int cluster, const char* what, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...), what);
+}
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Error bits written to the device error word.
@@ -77,6 +99,17 @@ __device__ __forceinline__ float bf2f(__nv_bfloat16 v) { return __bfloat162float
 // uses this one expression, so equal logits give equal keys everywhere.
 __device__ __forceinline__ float router_affinity(float x) {
   return __fdividef(1.0f, 1.0f + __expf(-x));
+}
+
+// Programmatic dependent launch: a kernel started with launch_after() may
+// begin while the stream's previous kernel still runs; pdl_wait() returns when
+// that kernel has completed and its writes are visible, so it comes before any
+// access to memory that earlier work touches.  pdl_trigger() in the earlier
+// kernel lets the next one begin once every block of the earlier one has
+// started.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Row range [r0, r1) of group g from the caller's offsets, clamped so that

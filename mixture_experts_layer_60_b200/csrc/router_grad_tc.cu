@@ -120,6 +120,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
+  pdl_wait();                  // d_logit's planes; the setup above overlaps their kernel
+  pdl_trigger();
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t full0 = map_shared_to(smem_u32(&full[0]), 0);
   const uint32_t tempty0 = map_shared_to(smem_u32(&tempty[0]), 0);
@@ -270,6 +272,7 @@ __global__ void __launch_bounds__(256) router_de_join_kernel(const float* __rest
                                                              int N_r, int d,
                                                              float* __restrict__ dE) {
   __shared__ int s_c0, s_c1;
+  pdl_wait();
   const int tile = blockIdx.x, slab = tile % n_slab, e0 = tile / n_slab * 256;
   if (threadIdx.x == 0) {
     // the pairs whose runs meet the tile's units
@@ -379,6 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
+  pdl_wait();                  // d_logit's planes; the setup above overlaps their kernel
+  pdl_trigger();
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t full0 = map_shared_to(smem_u32(&full[0]), 0);
   const uint32_t afull0 = map_shared_to(smem_u32(afull), 0);
@@ -583,19 +588,7 @@ moe_status launch_pairs(void (*kern)(Params...), long long pairs, int smem, bool
                         const char* what, cudaStream_t s, const Args&... args) {
   const moe_status st = ensure_max_smem(reinterpret_cast<const void*>(kern), smem, attr_done, what);
   if (st != MOE_OK) return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * (unsigned)pairs);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, kern, args...), what);
+  return launch_after(kern, dim3(2 * (unsigned)pairs), dim3(kThreads), smem, s, 2, what, args...);
 }
 
 // Pairs that share dE's units: all of the GPU's, but none with fewer than two.
@@ -682,9 +675,8 @@ moe_status launch_router_grad_tc(const void* u, const void* E, int T, int d, int
   if (st != MOE_OK) return st;
   const int rows = N_r < 256 ? N_r : 256;
   const dim3 grid(p.n_et * p.n_slab, (rows + kJoinRows - 1) / kJoinRows);
-  router_de_join_kernel<<<grid, 256, 0, s>>>(p.C, p.n_pairs, p.nk, p.n_slab,
-                                            p.n_et * p.n_slab * p.nk, N_r, d, dE);
-  return cuda_check(cudaGetLastError(), "router_de_join launch");
+  return launch_after(router_de_join_kernel, grid, dim3(256), 0, s, 1, "router_de_join launch", p.C,
+                      p.n_pairs, p.nk, p.n_slab, p.n_et * p.n_slab * p.nk, N_r, d, dE);
 }
 
 }  // namespace moe

@@ -37,7 +37,7 @@ __device__ __forceinline__ float wmax(float v) {
 
 // s = Sigmoid(x) and om = 1 - s, both to full relative precision.
 __device__ __forceinline__ void sigmoid_pair(float x, float& s, float& om) {
-  const float e = expf(x < 0.f ? x : -x), inv = 1.f / (1.f + e);
+  const float e = expf(x < 0.f ? x : -x), inv = __fdividef(1.f, 1.f + e);
   s = x < 0.f ? e * inv : inv;
   om = x < 0.f ? inv : e * inv;
 }
@@ -59,120 +59,180 @@ __device__ __forceinline__ int seq_at(const int32_t* off, int n_seq, int t) {
   return lo;
 }
 
-constexpr int kChunk = 32;       // tokens per block of the balance sums
-constexpr int kBalWarps = 8;
+constexpr int kChunk = 64;       // tokens per block of the balance sums
 
 // Partial sums of one (chunk of tokens, sequence) pair, row chunk + sequence:
-// along the pairs either number grows, so the rows are distinct.  Warp w takes
-// the pair's tokens w, w + 8, ...; the warps' sums are added in warp order.
-template <int V>
-__global__ void __launch_bounds__(32 * kBalWarps) balance_partial_kernel(
+// along the pairs either number grows, so the rows are distinct.  Each of W
+// warps takes U tokens at a time (their loads and reductions overlap: a token
+// alone is a chain of latencies), warps and tokens in a fixed order.  Reads
+// each logit once.
+template <int V, int W>
+__global__ void __launch_bounds__(32 * W) balance_partial_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ idx,
     const int32_t* __restrict__ off, int n_seq, int T, int N, int K, int softmax,
-    float* __restrict__ psum, int32_t* __restrict__ pcnt) {
-  extern __shared__ float sm[];                 // [kBalWarps][N] sums, then [N] counts
-  int* cnt = reinterpret_cast<int*>(sm + kBalWarps * N);
+    float2* __restrict__ part) {
+  constexpr int U = V <= 2 ? 4 : V <= 8 ? 2 : 1;
+  extern __shared__ float sm[];                 // [W][N] sums, then [N] counts
+  int* cnt = reinterpret_cast<int*>(sm + W * N);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_trigger();
   const int t0 = blockIdx.x * kChunk, t1 = min(T, t0 + kChunk);
-  int q = seq_at(off, n_seq, t0);
+  // the sequence of the chunk's first token: offsets counted side by side (a
+  // search is a chain of dependent loads), unless there are very many
+  int q;
+  if (off && n_seq <= 4096) {
+    int c = 0;
+    for (int i0 = 0; i0 < n_seq; i0 += 32 * W) {
+      const int i = i0 + threadIdx.x;
+      c += __syncthreads_count(i < n_seq && off[i] <= t0);
+    }
+    q = c - 1;
+  } else {
+    q = seq_at(off, n_seq, t0);
+  }
   if (q < 0) q = 0;
   for (; q < n_seq; ++q) {
     int r0, r1;
     seq_range(off, q, T, nullptr, r0, r1);
     if (r0 >= t1) break;
+    const bool last = r1 >= t1;                 // the next sequence starts in a later chunk
     r0 = max(r0, t0);
     r1 = min(r1, t1);
     if (r0 >= r1) continue;
     for (int i = threadIdx.x; i < N; i += blockDim.x) cnt[i] = 0;
-    __syncthreads();
     float acc[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.f;
-    for (int t = r0 + warp; t < r1; t += kBalWarps) {
-      float s[V], m = -INFINITY, z = 0.f;
+    __syncthreads();
+    for (int tb = r0 + warp * U; tb < r1; tb += W * U) {
+      float s[U][V], z[U], m[U];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int e = j * 32 + lane;
-        s[j] = e < N ? logits[(size_t)t * N + e] : -INFINITY;
-        m = fmaxf(m, s[j]);
-      }
-      if (softmax) m = wmax(m);
+      for (int c = 0; c < U; ++c) {
+        m[c] = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if (j * 32 + lane < N) {
-          float om;
-          if (softmax) s[j] = expf(s[j] - m);
-          else sigmoid_pair(s[j], s[j], om);
-          z += s[j];
-        } else {
-          s[j] = 0.f;
+        for (int j = 0; j < V; ++j) {
+          const int e = j * 32 + lane;
+          s[c][j] = tb + c < r1 && e < N ? logits[(size_t)(tb + c) * N + e] : -INFINITY;
+          m[c] = fmaxf(m[c], s[c][j]);
         }
       }
-      const float inv = 1.f / wsum(z);
-#pragma unroll
-      for (int j = 0; j < V; ++j) acc[j] = fmaf(s[j], inv, acc[j]);
-      for (int k = lane; k < K; k += 32) {
-        const int e = idx[(size_t)t * K + k];
+      // the tokens' slots: whole numbers, in any order
+      const int nk = min(U, r1 - tb) * K;
+      for (int k = lane; k < nk; k += 32) {
+        const int e = idx[(size_t)tb * K + k];
         if (e >= 0 && e < N) atomicAdd(&cnt[e], 1);
+      }
+      if (softmax) {
+#pragma unroll
+        for (int c = 0; c < U; ++c) m[c] = wmax(m[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < U; ++c) {
+        z[c] = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          if (tb + c < r1 && j * 32 + lane < N) {
+            float om;
+            if (softmax) s[c][j] = expf(s[c][j] - m[c]);
+            else sigmoid_pair(s[c][j], s[c][j], om);
+            z[c] += s[c][j];
+          } else {
+            s[c][j] = 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < U; ++c) z[c] = wsum(z[c]);
+#pragma unroll
+      for (int c = 0; c < U; ++c) {
+        const float inv = tb + c < r1 ? 1.f / z[c] : 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = fmaf(s[c][j], inv, acc[j]);
       }
     }
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (j * 32 + lane < N) sm[warp * N + j * 32 + lane] = acc[j];
     __syncthreads();
-    const size_t row = (size_t)(blockIdx.x + q) * N;
+    float2* row = part + (size_t)(blockIdx.x + q) * N;
     for (int i = threadIdx.x; i < N; i += blockDim.x) {
       float a = 0.f;
 #pragma unroll
-      for (int w = 0; w < kBalWarps; ++w) a += sm[w * N + i];
-      psum[row + i] = a;
-      pcnt[row + i] = cnt[i];
+      for (int w = 0; w < W; ++w) a += sm[w * N + i];
+      row[i] = make_float2(a, __int_as_float(cnt[i]));
     }
+    if (last) break;
     __syncthreads();
   }
 }
 
-// One block per sequence: coef and loss from the partial rows in chunk order,
-// the sums over chunks in float64.
-__global__ void __launch_bounds__(256) balance_final_kernel(
-    const float* __restrict__ psum, const int32_t* __restrict__ pcnt,
-    const int32_t* __restrict__ off, int T, int N, int K, float alpha, float* __restrict__ loss,
-    float* __restrict__ coef, int* err) {
-  __shared__ double red[8];
-  const int q = blockIdx.x;
+// One block per sequence: coef and loss from the partial rows.  The block's
+// threads are groups of `cols` columns (a power of two); group g sums rows
+// g, g + groups, ... in float64, and the groups' sums join in group order.
+constexpr int kFinalThreads = 1024;
+__global__ void __launch_bounds__(kFinalThreads) balance_final_kernel(
+    const float2* __restrict__ part, const int32_t* __restrict__ off, int T, int N, int K,
+    int cols, float alpha, float* __restrict__ loss, float* __restrict__ coef, int* err) {
+  __shared__ double red[32];
+  __shared__ double sp[kFinalThreads];
+  __shared__ int sc[kFinalThreads];
+  const int q = blockIdx.x, g = threadIdx.x / cols, i = threadIdx.x % cols;
+  const int groups = kFinalThreads / cols;
+  pdl_wait();
   int r0, r1;
   seq_range(off, q, T, threadIdx.x == 0 ? err : nullptr, r0, r1);
   const int n = r1 - r0;
-  double part = 0.0;
-  for (int i = threadIdx.x; i < N; i += blockDim.x) {
-    double p = 0.0;
-    int c = 0;
-    if (n > 0)
-      for (int k = r0 / kChunk; k <= (r1 - 1) / kChunk; ++k) {
-        p += (double)psum[(size_t)(k + q) * N + i];
-        c += pcnt[(size_t)(k + q) * N + i];
-      }
+  double p = 0.0;
+  int c = 0;
+  if (n > 0 && i < N) {
+    const float2* row = part + (size_t)q * N + i;
+    const int k1 = (r1 - 1) / kChunk;
+#pragma unroll 4
+    for (int k = r0 / kChunk + g; k <= k1; k += groups) {
+      const float2 v = row[(size_t)k * N];
+      p += (double)v.x;
+      c += __float_as_int(v.y);
+    }
+  }
+  sp[threadIdx.x] = p;
+  sc[threadIdx.x] = c;
+  __syncthreads();
+  double term = 0.0;
+  if (g == 0 && i < N) {
+    for (int k = 1; k < groups; ++k) {
+      p += sp[k * cols + i];
+      c += sc[k * cols + i];
+    }
     // alpha f_i / n with f_i = N_r c / (K n): rounded once
     const double cf = n > 0 ? (double)alpha * N * c / ((double)K * n * n) : 0.0;
     coef[(size_t)q * N + i] = (float)cf;
-    part += cf * p;
+    term = cf * p;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = part;
+  for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = term;
   __syncthreads();
   if (threadIdx.x == 0) {
     double a = 0.0;
-    for (int w = 0; w < 8; ++w) a += red[w];
+    for (int w = 0; w < kFinalThreads / 32; ++w) a += red[w];
     loss[q] = (float)a;
   }
 }
 
 // ---------------------------------------------------------------- logit gradient
-// A warp per token.  planes: d_logit as bf16 planes too (router_grad_tc.cu).
+// A warp per token, bound by the logits, planes and d_logit it moves and by
+// some 600 instructions a token.  planes: d_logit as bf16 planes too
+// (router_grad_tc.cu).  PAIR: a lane holds two neighbouring experts of every
+// 64 (8-byte loads and stores, rounded two at a time) where N_r is even and
+// the rows are 8-byte aligned; else one of every 32.
 constexpr int kGradWarps = 4;
 
-template <int V>
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int V, bool PAIR>
 __global__ void __launch_bounds__(32 * kGradWarps) router_logit_grad_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ idx,
     const float* __restrict__ d_gate, const int32_t* __restrict__ off, int n_seq,
@@ -180,6 +240,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_logit_grad_kernel(
     int softmax, int renorm, float scale, float* __restrict__ d_logit,
     __nv_bfloat16* __restrict__ planes, int Tp, int Np) {
   extern __shared__ float sm[];
+  pdl_trigger();
   // the planes' rows past the last token
   if (planes) {
     const long long pad = (long long)(Tp - T) * Np;
@@ -188,22 +249,39 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_logit_grad_kernel(
       planes[((i / pad) * Tp + T) * (long long)Np + i % pad] = __float2bfloat16_rn(0.f);
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* row = sm + (size_t)warp * N;          // the token's scores, then its slots' terms
+  float* row = sm + (size_t)warp * N;          // the slots' terms by expert
+  const auto expert = [&](int j) { return PAIR ? (j >> 1) * 64 + 2 * lane + (j & 1) : j * 32 + lane; };
   for (int t = blockIdx.x * kGradWarps + warp; t < T; t += gridDim.x * kGradWarps) {
-    float x[V], s[V], om[V], q[V], m = -INFINITY, z = 0.f;
+    const float* lrow = logits + (size_t)t * N;
+    // the slot of this lane (K <= 32: one; else the loops below come back)
+    float s[V], om[V], m = -INFINITY, z = 0.f;
+    if (PAIR) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int e = j * 32 + lane;
-      x[j] = e < N ? logits[(size_t)t * N + e] : -INFINITY;
-      m = fmaxf(m, x[j]);
-      q[j] = 0.f;
+      for (int j = 0; j < V; j += 2) {
+        const int e = expert(j);
+        const float2 v = e < N ? *reinterpret_cast<const float2*>(lrow + e)
+                               : make_float2(-INFINITY, -INFINITY);
+        s[j] = v.x;
+        s[j + 1 < V ? j + 1 : j] = v.y;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[j] = expert(j) < N ? lrow[expert(j)] : -INFINITY;
     }
-    if (softmax) m = wmax(m);
+    if (d_gate)
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (expert(j) < N) row[expert(j)] = 0.f;
+    if (softmax) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) m = fmaxf(m, s[j]);
+      m = wmax(m);
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      if (j * 32 + lane < N) {
-        if (softmax) { s[j] = expf(x[j] - m); om[j] = 1.f; }
-        else sigmoid_pair(x[j], s[j], om[j]);
+      if (expert(j) < N) {
+        if (softmax) { s[j] = expf(s[j] - m); om[j] = 1.f; }
+        else sigmoid_pair(s[j], s[j], om[j]);
         z += s[j];
       } else {
         s[j] = 0.f;
@@ -216,7 +294,9 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_logit_grad_kernel(
       for (int j = 0; j < V; ++j) s[j] *= inv;
     }
     // balance term
-    float Q = 0.f;
+    float q[V], Q = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) q[j] = 0.f;
     if (coef) {
       const int sq = seq_at(off, n_seq, t);
       int r0 = 0, r1 = 0;
@@ -225,114 +305,122 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_logit_grad_kernel(
         const float dl = d_loss ? d_loss[sq] : 1.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const int e = j * 32 + lane;
-          if (e < N) q[j] = dl * coef[(size_t)sq * N + e];
+          if (expert(j) < N) q[j] = dl * coef[(size_t)sq * N + expert(j)];
           Q = fmaf(s[j], q[j], Q);
         }
         Q = wsum(Q);
         if (!softmax) Q *= inv;
       }
     }
-    // the slots
+    // the slots' terms, by expert
     float R = 0.f;
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (j * 32 + lane < N) row[j * 32 + lane] = x[j];
-    __syncwarp();
-    float xm = -INFINITY, den = 1.f, G = 0.f;
-    bool ratio = false;
-    float sxm = 1.f, dum;
-    const auto slot = [&](int k, int& e, float& dg) {      // expert (-1: left out) and d_gate
-      e = idx[(size_t)t * K + k];
-      if (e < 0 || e >= N) e = -1;
-      dg = e >= 0 ? scale * d_gate[(size_t)t * K + k] : 0.f;
-    };
-    const auto weight = [&](float xk) {                    // the score over the largest one
-      if (!ratio) return expf(xk - xm);
-      float a, b;
-      sigmoid_pair(xk, a, b);
-      return a / sxm;
-    };
-    if (d_gate && renorm) {
-      for (int k = lane; k < K; k += 32) {
-        int e;
-        float dg;
-        slot(k, e, dg);
-        if (e >= 0) { const float v = row[e]; xm = v > xm || v != v ? v : xm; }
-      }
-      xm = wmax(xm);
-      ratio = !softmax && !(xm < -30.f);
-      if (ratio) sigmoid_pair(xm, sxm, dum);
-      float w = 0.f, wd = 0.f;
-      for (int k = lane; k < K; k += 32) {
-        int e;
-        float dg;
-        slot(k, e, dg);
-        if (e >= 0) {
-          const float v = weight(row[e]);
-          w += v;
-          wd = fmaf(v, dg, wd);
-        }
-      }
-      den = wsum(w);
-      G = wsum(wd) / den;
-    }
-    float mine_v = 0.f;
-    int mine_e = -1;
-    // terms of the slots, then added to the row in slot order (an expert may
-    // come twice)
-    float add[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) add[j] = 0.f;
     if (d_gate) {
-      for (int k0 = 0; k0 < K; k0 += 32) {
-        mine_e = -1;
-        mine_v = 0.f;
-        if (k0 + lane < K) {
-          float dg;
-          slot(k0 + lane, mine_e, dg);
-          if (mine_e >= 0) {
-            const float xk = row[mine_e];
-            float a, b;
-            if (softmax) { a = expf(xk - m) * inv; b = 1.f; }
-            else sigmoid_pair(xk, a, b);
-            if (renorm) mine_v = weight(xk) / den * b * (dg - G);
-            else { mine_v = a * b * dg; R += softmax ? a * dg : 0.f; }
+      const auto slot = [&](int k, int& e, float& dg, float& x) {   // e < 0: left out
+        e = k < K ? idx[(size_t)t * K + k] : -1;
+        if (e >= N) e = -1;
+        dg = e >= 0 ? scale * d_gate[(size_t)t * K + k] : 0.f;
+        x = e >= 0 ? lrow[e] : -INFINITY;
+      };
+      int e = -1;
+      float dg = 0.f, x = -INFINITY, xm = -INFINITY, sxm = 1.f, den = 1.f, G = 0.f, dum;
+      bool ratio = false;
+      const auto weight = [&](float v) {                   // the score over the largest one
+        if (!ratio) return expf(v - xm);
+        float a, b;
+        sigmoid_pair(v, a, b);
+        return __fdividef(a, sxm);
+      };
+      if (renorm) {
+        for (int k0 = 0; k0 < K; k0 += 32) {
+          slot(k0 + lane, e, dg, x);
+          if (e >= 0) xm = x > xm || x != x ? x : xm;
+        }
+        xm = wmax(xm);
+        ratio = !softmax && !(xm < -30.f);
+        if (ratio) sigmoid_pair(xm, sxm, dum);
+        float w = 0.f, wd = 0.f;
+        for (int k0 = 0; k0 < K; k0 += 32) {
+          if (K > 32) slot(k0 + lane, e, dg, x);
+          if (e >= 0) {
+            const float v = weight(x);
+            w += v;
+            wd = fmaf(v, dg, wd);
           }
         }
-        const int kn = min(32, K - k0);
-        for (int k = 0; k < kn; ++k) {
-          const int e = __shfl_sync(0xffffffffu, mine_e, k);
-          const float v = __shfl_sync(0xffffffffu, mine_v, k);
-#pragma unroll
-          for (int j = 0; j < V; ++j)
-            if (e == j * 32 + lane) add[j] += v;
+        den = wsum(w);
+        G = wsum(wd) / den;
+      }
+      for (int k0 = 0; k0 < K; k0 += 32) {
+        if (K > 32 || !renorm) slot(k0 + lane, e, dg, x);
+        float v = 0.f;
+        if (e >= 0) {
+          float a, b;
+          if (softmax) { a = expf(x - m) * inv; b = 1.f; }
+          else sigmoid_pair(x, a, b);
+          if (renorm) v = weight(x) / den * b * (dg - G);
+          else { v = a * b * dg; R += softmax ? v : 0.f; }
+        }
+        __syncwarp();
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        if (__all_sync(0xffffffffu, e < 0 || (same & (same - 1u)) == 0u)) {
+          if (e >= 0) row[e] += v;
+        } else {
+          // an expert more than once: its slots one after the other
+          for (int k = 0; k < 32; ++k) {
+            if (lane == k && e >= 0) row[e] += v;
+            __syncwarp();
+          }
         }
       }
       R = wsum(R);
+      __syncwarp();
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int e = j * 32 + lane;
-      if (e < N) {
-        const float dense = softmax ? s[j] * (q[j] - Q - R) : s[j] * om[j] * (q[j] - Q) * inv;
-        add[j] += dense;
-        if (d_logit) d_logit[(size_t)t * N + e] = add[j];
-      } else {
-        add[j] = 0.f;
+      const int e = expert(j);
+      float v = softmax ? s[j] * (q[j] - Q - R) : s[j] * om[j] * (q[j] - Q) * inv;
+      if (d_gate && e < N) v += row[e];
+      s[j] = e < N ? v : 0.f;
+    }
+    __syncwarp();                                  // the row is rewritten for the next token
+    if (PAIR) {
+#pragma unroll
+      for (int j = 0; j < V; j += 2) {
+        constexpr int last = V - 1;
+        const int e = expert(j), j1 = j + 1 <= last ? j + 1 : j;
+        if (d_logit && e < N)
+          *reinterpret_cast<float2*>(d_logit + (size_t)t * N + e) = make_float2(s[j], s[j1]);
+        if (planes && e < Np) {
+          // hi + mid + lo: 24 bits in three roundings; an infinity stays in hi
+          const uint32_t hi = bf16x2(s[j], s[j1]);
+          const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xffff0000u);
+          const float a0 = fabsf(h0) < INFINITY ? s[j] - h0 : 0.f;
+          const float a1 = fabsf(h1) < INFINITY ? s[j1] - h1 : 0.f;
+          const uint32_t mid = bf16x2(a0, a1);
+          const uint32_t lo = bf16x2(a0 - __uint_as_float(mid << 16),
+                                     a1 - __uint_as_float(mid & 0xffff0000u));
+          uint32_t* at = reinterpret_cast<uint32_t*>(planes + (size_t)t * Np + e);
+          const size_t plane = (size_t)Tp * Np / 2;
+          at[0] = hi;
+          at[plane] = mid;
+          at[2 * plane] = lo;
+        }
       }
-      if (planes && e < Np) {
-        // hi + mid + lo: 24 bits in three roundings; an infinity stays in hi
-        const __nv_bfloat16 hi = __float2bfloat16_rn(add[j]);
-        const float fh = __bfloat162float(hi);
-        const float r1 = fabsf(fh) < INFINITY ? add[j] - fh : 0.f;
-        const __nv_bfloat16 mid = __float2bfloat16_rn(r1);
-        const __nv_bfloat16 lo = __float2bfloat16_rn(r1 - __bfloat162float(mid));
-        const size_t at = (size_t)t * Np + e, plane = (size_t)Tp * Np;
-        planes[at] = hi;
-        planes[at + plane] = mid;
-        planes[at + 2 * plane] = lo;
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int e = expert(j);
+        if (d_logit && e < N) d_logit[(size_t)t * N + e] = s[j];
+        if (planes && e < Np) {
+          const __nv_bfloat16 hi = __float2bfloat16_rn(s[j]);
+          const float fh = __bfloat162float(hi);
+          const float r1 = fabsf(fh) < INFINITY ? s[j] - fh : 0.f;
+          const __nv_bfloat16 mid = __float2bfloat16_rn(r1);
+          const size_t at = (size_t)t * Np + e, plane = (size_t)Tp * Np;
+          planes[at] = hi;
+          planes[at + plane] = mid;
+          planes[at + 2 * plane] = __float2bfloat16_rn(r1 - __bfloat162float(mid));
+        }
       }
     }
   }
@@ -399,38 +487,39 @@ int dispatch_v(int N) {
 
 }  // namespace
 
-// Partial rows: one for every (chunk, sequence) pair.
+// Partial rows (sum and count of every expert): one for every (chunk,
+// sequence) pair.
 size_t balance_ws_bytes(int T, int N_r, int n_seq) {
   const size_t rows = (size_t)(T + kChunk - 1) / kChunk + n_seq;
-  return 2 * align_up(rows * N_r * 4, 256);
+  return align_up(rows * N_r * sizeof(float2), 256);
 }
 
 moe_status launch_balance_loss(const float* logits, const int32_t* idx, const int32_t* off,
                                int n_seq, int T, int N_r, int K, int score, float alpha,
                                float* loss, float* coef, void* ws, cudaStream_t s) {
-  float* psum = static_cast<float*>(ws);
-  int32_t* pcnt = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) +
-                                             balance_ws_bytes(T, N_r, n_seq) / 2);
+  float2* part = static_cast<float2*>(ws);
   int* err = device_error_word();
   if (!err) return fail(MOE_ERR_CUDA, "device error word unavailable");
   const int softmax = score == MOE_SCORE_SOFTMAX;
-  const size_t smem = (size_t)(kBalWarps + 1) * N_r * 4;
   const int blocks = (T + kChunk - 1) / kChunk;
-#define MOE_BAL(v)                                                                            \
+  // sums of W warps and the counts in at most 36 KB
+#define MOE_BAL(v, w)                                                                         \
   case v:                                                                                     \
-    balance_partial_kernel<v><<<blocks, 32 * kBalWarps, smem, s>>>(                           \
-        logits, idx, off, n_seq, T, N_r, K, softmax, psum, pcnt);                             \
+    balance_partial_kernel<v, w><<<blocks, 32 * w, (size_t)(w + 1) * N_r * 4, s>>>(           \
+        logits, idx, off, n_seq, T, N_r, K, softmax, part);                                   \
     break;
   if (blocks > 0) {
     switch (dispatch_v(N_r)) {
-      MOE_BAL(1) MOE_BAL(2) MOE_BAL(4) MOE_BAL(8) MOE_BAL(16) MOE_BAL(32)
+      MOE_BAL(1, 16) MOE_BAL(2, 16) MOE_BAL(4, 16) MOE_BAL(8, 32) MOE_BAL(16, 16) MOE_BAL(32, 8)
     }
     const moe_status st = cuda_check(cudaGetLastError(), "balance_partial launch");
     if (st != MOE_OK) return st;
   }
 #undef MOE_BAL
-  balance_final_kernel<<<n_seq, 256, 0, s>>>(psum, pcnt, off, T, N_r, K, alpha, loss, coef, err);
-  return cuda_check(cudaGetLastError(), "balance_final launch");
+  int cols = 32;
+  while (cols < N_r) cols *= 2;
+  return launch_after(balance_final_kernel, dim3(n_seq), dim3(kFinalThreads), 0, s, 1,
+                      "balance_final launch", part, off, T, N_r, K, cols, alpha, loss, coef, err);
 }
 
 size_t route_scored_bwd_ws_bytes(moe_dtype dt, int T, int d, int N_r) {
@@ -452,15 +541,21 @@ moe_status launch_route_scored_backward(const void* u, const void* E, moe_dtype 
   int blocks = (T + kGradWarps - 1) / kGradWarps;
   const size_t smem = (size_t)kGradWarps * N_r * 4;
   const int softmax = score == MOE_SCORE_SOFTMAX;
+  const bool pair = N_r % 2 == 0 && N_r > 32 && reinterpret_cast<uintptr_t>(logits) % 8 == 0 &&
+                    reinterpret_cast<uintptr_t>(d_logit) % 8 == 0;
+#define MOE_GRAD_RUN(v, p)                                                                    \
+  router_logit_grad_kernel<v, p><<<blocks, 32 * kGradWarps, smem, s>>>(                       \
+      logits, idx, d_gate, off, n_seq, coef, d_loss, T, N_r, K, softmax, renorm, scale, dl,   \
+      planes, pl.Tp, pl.Np)
 #define MOE_GRAD(v)                                                                           \
   case v:                                                                                     \
-    router_logit_grad_kernel<v><<<blocks, 32 * kGradWarps, smem, s>>>(                        \
-        logits, idx, d_gate, off, n_seq, coef, d_loss, T, N_r, K, softmax, renorm, scale, dl,  \
-        planes, pl.Tp, pl.Np);                                                                \
+    if (pair) MOE_GRAD_RUN(v, (v > 1));                                                       \
+    else MOE_GRAD_RUN(v, false);                                                              \
     break;
   switch (dispatch_v(N_r)) {
     MOE_GRAD(1) MOE_GRAD(2) MOE_GRAD(4) MOE_GRAD(8) MOE_GRAD(16) MOE_GRAD(32)
   }
+#undef MOE_GRAD_RUN
 #undef MOE_GRAD
   moe_status st = cuda_check(cudaGetLastError(), "router_logit_grad launch");
   if (st != MOE_OK) return st;

@@ -62,7 +62,7 @@ struct LogitParams {
   int ld;                   // n_et * Nt
   float* P;                 // [S][T][ld]
   int32_t* counts;          // zeroed here, as is the listing's length
-  int32_t* n_listed;
+  int32_t* n_listed;        // two lengths
   int* err;
 };
 
@@ -107,9 +107,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tmem2_alloc(tmem_slot, 512);
     tmem2_relinquish();
   }
+  pdl_trigger();
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i < p.N_r; i += blockDim.x) p.counts[i] = 0;
-    if (threadIdx.x == 0) *p.n_listed = 0;
+    if (threadIdx.x < 2) p.n_listed[threadIdx.x] = 0;
   }
   tc_fence_before();
   cluster_sync_all();          // barriers initialised in both CTAs, TMEM allocated
@@ -320,6 +321,7 @@ __global__ void __launch_bounds__(128) router_logits_few_kernel(
     double* __restrict__ P, int32_t* __restrict__ counts) {
   __shared__ double part[4][TT];
   const int e = blockIdx.x, tid = threadIdx.x, nv = d / 8;
+  pdl_trigger();
   if (e == 0)
     for (int i = tid; i < N; i += 128) counts[i] = 0;
   const uint4* er = reinterpret_cast<const uint4*>(E + (size_t)e * d);
@@ -379,6 +381,7 @@ __global__ void __launch_bounds__(256) router_logits64_kernel(
   __shared__ double su[kT64][kT64 + 1], se[kT64][kT64 + 1];
   const int tid = threadIdx.x;
   const int t0 = blockIdx.x * kT64, e0 = blockIdx.y * kT64, sl = blockIdx.z;
+  pdl_trigger();
   if (blockIdx.x == 0 && blockIdx.y == 0 && sl == 0)
     for (int i = tid; i < N; i += 256) counts[i] = 0;
   const int nc = d / kT64;                                // d % 64 == 0
@@ -417,10 +420,15 @@ __global__ void __launch_bounds__(256) router_logits64_kernel(
 // A warp per token; the block's load histogram in shared memory, then added to
 // counts (whole numbers: the order of the additions does not matter).
 
-// The tokens listed for the exact pass: how many, and their ids.
+// The tokens listed for the exact pass: how many, and their ids; and those of
+// them whose every logit has to be exact: how many, ids, finished shares and
+// float64 logits [T][N_r].
 struct Recheck {
-  int32_t* n;
+  int32_t* n;             // [2]
   int32_t* tok;
+  int32_t* full_tok;
+  int32_t* full_done;
+  double* full_x;
 };
 
 // x[j]: the slices' sums, joined in float64 and rounded once; returns the
@@ -461,6 +469,8 @@ __global__ void __launch_bounds__(128) router_select_kernel(
   float* wk = reinterpret_cast<float*>(hist + N) + (size_t)warp * N;
   for (int i = threadIdx.x; i < N; i += blockDim.x) hist[i] = 0;
   __syncthreads();
+  pdl_wait();
+  pdl_trigger();
   for (int t = blockIdx.x * wpb + warp; t < T; t += gridDim.x * wpb) {
     float x[V], sc[V], key[V];
     const float mag = sel_warp_max(join_slices<V>(P + (size_t)t * ld, S, (size_t)T * ld, N, x));
@@ -498,16 +508,17 @@ __global__ void __launch_bounds__(MAXT) router_token_kernel(
     const __nv_bfloat16* __restrict__ u, const __nv_bfloat16* __restrict__ E,
     const void* __restrict__ P, int S, int ld, const float* __restrict__ bias, int T, int d,
     SelectRule r, int32_t* __restrict__ idx, float* __restrict__ gate,
-    int32_t* __restrict__ counts, float* __restrict__ logits, const int32_t* __restrict__ n_listed,
-    const int32_t* __restrict__ listed) {
+    int32_t* __restrict__ counts, float* __restrict__ logits, Recheck rc, bool all_tokens) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ double part[MAXT / 32][kDots];
   __shared__ double red[33];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = r.N_r, nv = d / 8;
   const BlockRoute b = block_route_smem(smem_raw, N, r.K);
-  const int n = listed ? *n_listed : T;
+  pdl_wait();
+  pdl_trigger();
+  const int n = all_tokens ? T : rc.n[0];
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
-    const int t = listed ? listed[i] : i;
+    const int t = all_tokens ? i : rc.tok[i];
     double a = 0.0, mag = 0.0;
     if (tid < N) {
       const size_t at = (size_t)t * ld + tid, stride = (size_t)T * ld;
@@ -572,8 +583,79 @@ __global__ void __launch_bounds__(MAXT) router_token_kernel(
         __syncthreads();
       }
     };
-    block_route(b, r, bias, logit_err, fetch, idx + (size_t)t * r.K, gate + (size_t)t * r.K,
-                counts);
+    const bool done = block_route(b, r, bias, logit_err, fetch, idx + (size_t)t * r.K,
+                                  gate + (size_t)t * r.K, counts);
+    if (!done && tid == 0) {
+      const int slot = atomicAdd(&rc.n[1], 1);
+      rc.full_tok[slot] = t;
+      rc.full_done[slot] = 0;
+    }
+    __syncthreads();
+  }
+}
+
+// The tokens whose every logit has to be exact (softmax scores a rounding
+// apart: one token of some 30000).  A share is one expert for each warp of a
+// block, so a lone token's N_r dot products spread over the GPU (by one block
+// they took 200 us); the block that finishes a token's last share routes it.
+template <int MAXT>
+__global__ void __launch_bounds__(MAXT) router_full_kernel(
+    const __nv_bfloat16* __restrict__ u, const __nv_bfloat16* __restrict__ E,
+    const float* __restrict__ bias, int d, SelectRule r, int32_t* __restrict__ idx,
+    float* __restrict__ gate, int32_t* __restrict__ counts, Recheck rc) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ int last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = r.N_r, nv = d / 8;
+  const int per = blockDim.x >> 5, shares = (N + per - 1) / per;
+  const BlockRoute b = block_route_smem(smem_raw, N, r.K);
+  pdl_wait();
+  const long long work = (long long)rc.n[1] * shares;
+  for (long long w = blockIdx.x; w < work; w += gridDim.x) {
+    const int i = (int)(w / shares), e = (int)(w - (long long)i * shares) * per + warp;
+    const int t = rc.full_tok[i];
+    if (e < N) {
+      const uint4* ur = reinterpret_cast<const uint4*>(u + (size_t)t * d);
+      const uint4* er = reinterpret_cast<const uint4*>(E + (size_t)e * d);
+      double a = 0.0, c = 0.0;
+      constexpr int U = 4;
+      for (int v0 = lane; v0 < nv; v0 += 32 * U) {
+        uint4 x[U], y[U];
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          const int v = v0 + 32 * q;
+          x[q] = v < nv ? __ldg(ur + v) : make_uint4(0, 0, 0, 0);
+          y[q] = v < nv ? __ldg(er + v) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          float fx[8], fy[8];
+          Vec<__nv_bfloat16>::load(x[q], fx);
+          Vec<__nv_bfloat16>::load(y[q], fy);
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            a += (double)(fx[k] * fy[k]);
+            c += (double)(fx[k + 1] * fy[k + 1]);
+          }
+        }
+      }
+      a = sel_warp_sum(a + c);
+      if (lane == 0) {
+        rc.full_x[(size_t)i * N + e] = a;
+        __threadfence();
+      }
+    }
+    __syncthreads();
+    if (tid == 0) last = atomicAdd(&rc.full_done[i], 1) == shares - 1;
+    __syncthreads();
+    if (last) {
+      __threadfence();
+      if (tid < N) {
+        b.x[tid] = __ldcg(rc.full_x + (size_t)i * N + tid);
+        b.exact_f[tid] = 1;
+      }
+      block_route(b, r, bias, 0.f, [](int) {}, idx + (size_t)t * r.K, gate + (size_t)t * r.K,
+                  counts);
+    }
     __syncthreads();
   }
 }
@@ -600,10 +682,14 @@ size_t tc_ws_bytes(int T, int d, int N, Recheck* rc, uint8_t* base) {
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes, 256); return at; };
   take((size_t)L.S * T * L.ld * 4);
-  const size_t n = take(4), tok = take((size_t)T * 4);
+  const size_t n = take(8), tok = take((size_t)T * 4), ftok = take((size_t)T * 4),
+               fdone = take((size_t)T * 4), fx = take((size_t)T * N * 8);
   if (rc) {
     rc->n = reinterpret_cast<int32_t*>(base + n);
     rc->tok = reinterpret_cast<int32_t*>(base + tok);
+    rc->full_tok = reinterpret_cast<int32_t*>(base + ftok);
+    rc->full_done = reinterpret_cast<int32_t*>(base + fdone);
+    rc->full_x = reinterpret_cast<double*>(base + fx);
   }
   return o;
 }
@@ -668,21 +754,27 @@ namespace {
 template <bool EXACT>
 moe_status launch_router_token(const void* u, const void* E, const void* P, int S, int ld,
                                const float* b, int T, int d, const SelectRule& r, int32_t* idx,
-                               float* gate, int32_t* counts, float* logits,
-                               const int32_t* n_listed, const int32_t* listed, int blocks,
-                               cudaStream_t s) {
+                               float* gate, int32_t* counts, float* logits, const Recheck& rc,
+                               bool all_tokens, int blocks, cudaStream_t s) {
   int threads = (r.N_r + 31) / 32 * 32;
   if (threads < 128) threads = 128;
   const size_t smem = block_route_bytes(r.N_r, r.K);
   const auto ub = static_cast<const __nv_bfloat16*>(u);
   const auto eb = static_cast<const __nv_bfloat16*>(E);
-  if (threads <= 256)
-    router_token_kernel<EXACT, 256><<<blocks, threads, smem, s>>>(
-        ub, eb, P, S, ld, b, T, d, r, idx, gate, counts, logits, n_listed, listed);
-  else
-    router_token_kernel<EXACT, 1024><<<blocks, threads, smem, s>>>(
-        ub, eb, P, S, ld, b, T, d, r, idx, gate, counts, logits, n_listed, listed);
-  return cuda_check(cudaGetLastError(), "router_token launch");
+  const auto kern = threads <= 256 ? router_token_kernel<EXACT, 256> : router_token_kernel<EXACT, 1024>;
+  return launch_after(kern, dim3(blocks), dim3(threads), smem, s, 1, "router_token launch", ub, eb, P,
+                      S, ld, b, T, d, r, idx, gate, counts, logits, rc, all_tokens);
+}
+
+moe_status launch_router_full(const void* u, const void* E, const float* b, int d,
+                              const SelectRule& r, int32_t* idx, float* gate, int32_t* counts,
+                              const Recheck& rc, cudaStream_t s) {
+  int threads = (r.N_r + 31) / 32 * 32;
+  if (threads < 256) threads = 256;
+  const auto kern = threads <= 256 ? router_full_kernel<256> : router_full_kernel<1024>;
+  return launch_after(kern, dim3(sm_count()), dim3(threads), block_route_bytes(r.N_r, r.K), s, 1,
+                      "router_full launch", static_cast<const __nv_bfloat16*>(u),
+                      static_cast<const __nv_bfloat16*>(E), b, d, r, idx, gate, counts, rc);
 }
 }  // namespace
 
@@ -701,25 +793,30 @@ moe_status launch_route_scored(const void* u, const void* E, moe_dtype dt, const
     const LogitTiling L = logit_tiling(T, d, N_r);
     st = launch_logits_tc(u, E, T, d, N_r, P, counts, rc.n, s);
     if (st != MOE_OK) return st;
-    if (T <= kBlockTokens)
-      return launch_router_token<false>(u, E, P, L.S, L.ld, b, T, d, r, idx, gate, counts, logits,
-                                        nullptr, nullptr, T, s);
+    // a sigmoid needs no other logit: only softmax tokens can ask for all of them
+    const bool full = score == MOE_SCORE_SOFTMAX;
+    if (T <= kBlockTokens) {
+      st = launch_router_token<false>(u, E, P, L.S, L.ld, b, T, d, r, idx, gate, counts, logits, rc,
+                                      true, T, s);
+      return st == MOE_OK && full ? launch_router_full(u, E, b, d, r, idx, gate, counts, rc, s) : st;
+    }
     const int wpb = 4, blocks = (T + wpb - 1) / wpb < 16 * sm_count() ? (T + wpb - 1) / wpb
                                                                       : 16 * sm_count();
     const size_t smem = (size_t)N_r * sizeof(int) * (1 + wpb);
 #define MOE_SELECT(v)                                                                        \
   case v:                                                                                    \
-    router_select_kernel<v><<<blocks, wpb * 32, smem, s>>>(P, L.S, L.ld, b, T, r, idx, gate, \
-                                                           counts, logits, rc);              \
+    st = launch_after(router_select_kernel<v>, dim3(blocks), dim3(wpb * 32), smem, s, 1,     \
+                      "router_select launch", P, L.S, L.ld, b, T, r, idx, gate, counts,      \
+                      logits, rc);                                                           \
     break;
     switch (dispatch_v(N_r)) {
       MOE_SELECT(1) MOE_SELECT(2) MOE_SELECT(4) MOE_SELECT(8) MOE_SELECT(16) MOE_SELECT(32)
     }
 #undef MOE_SELECT
-    st = cuda_check(cudaGetLastError(), "router_select launch");
     if (st != MOE_OK) return st;
-    return launch_router_token<false>(u, E, P, L.S, L.ld, b, T, d, r, idx, gate, counts, nullptr,
-                                      rc.n, rc.tok, 2 * sm_count(), s);
+    st = launch_router_token<false>(u, E, P, L.S, L.ld, b, T, d, r, idx, gate, counts, nullptr, rc,
+                                    false, 2 * sm_count(), s);
+    return st == MOE_OK && full ? launch_router_full(u, E, b, d, r, idx, gate, counts, rc, s) : st;
   }
   double* P = static_cast<double*>(ws);
   int S = 1;
@@ -740,8 +837,8 @@ moe_status launch_route_scored(const void* u, const void* E, moe_dtype dt, const
   st = cuda_check(cudaGetLastError(), "router float64 logits launch");
   if (st != MOE_OK) return st;
   const int blocks = T < 16 * sm_count() ? T : 16 * sm_count();
-  return launch_router_token<true>(u, E, P, S, N_r, b, T, d, r, idx, gate, counts, logits, nullptr,
-                                   nullptr, blocks, s);
+  return launch_router_token<true>(u, E, P, S, N_r, b, T, d, r, idx, gate, counts, logits, Recheck{},
+                                   true, blocks, s);
 }
 
 }  // namespace moe

@@ -71,7 +71,8 @@ struct SelectRule {
 
 // Bound on a float32 logit's error per unit of max(4, largest |logit|).  The
 // tensor-core sums are cut every 32 accumulation steps; over N(0,1) rows at
-// d = 7168 and 2048 their largest error is 1.6e-6 (kLogitError * 4 = 1e-5).
+// d = 512 to 16384 their largest error was 3.1e-6 with logits up to 5.2, where
+// this bound is 1.3e-5.
 constexpr float kLogitError = 2.5e-6f;
 
 // Per token: the softmax's largest logit and sum, and the error bound of its
@@ -346,13 +347,15 @@ __device__ __forceinline__ double block_reduce(double v, bool sum, double* red) 
   return sum ? sel_warp_sum(v) : sel_warp_max(v);
 }
 
-// Routes one token by the whole block (blockDim.x >= N, whole warps), from
-// b.x and b.exact_f; logit_err bounds the error of the inexact logits.
+// Routes one token by the whole block; false: exact scores that only the error
+// of the softmax's sum keeps apart, so that every logit has to be exact first
+// (nothing has been written).  blockDim.x >= N, whole warps; from b.x and
+// b.exact_f; logit_err bounds the error of the inexact logits.
 // fetch(n): fills b.x for the experts b.list[0, n) with their exact logits and
 // synchronises the block.  Its last reads of b are warp 0's: the caller
 // synchronises before it fills b again.
 template <typename Fetch>
-__device__ __forceinline__ void block_route(const BlockRoute& b, const SelectRule& r,
+__device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRule& r,
                                             const float* __restrict__ bias, float logit_err,
                                             Fetch fetch, int32_t* __restrict__ idx,
                                             float* __restrict__ gate,
@@ -473,13 +476,12 @@ __device__ __forceinline__ void block_route(const BlockRoute& b, const SelectRul
           atomicMax(&s_hi, k + 1);
         }
       }
-      z_open = __syncthreads_or(z_open);
+      if (__syncthreads_or(z_open)) return false;
       if (s_hi >= 0 && mine && !ex) {
         const float lo = b.top_key[s_hi], hi = b.top_key[s_lo - 1];
         const float pad = 3.f * err + 2.f * rel * fabsf(key);
         want = want || (key >= lo - pad && key <= hi + pad);
       }
-      want = want || (z_open && mine && !ex);
       open = __syncthreads_or(want);
     }
     if (!open) break;
@@ -494,7 +496,7 @@ __device__ __forceinline__ void block_route(const BlockRoute& b, const SelectRul
     idx[k] = id;
     atomicAdd(&counts[id], 1);
   }
-  if (e >= 32) return;
+  if (e >= 32) return true;
   const auto slot_x = [&](int k) { return b.x[b.top_id[k]]; };
   double xm = -INFINITY, sm = 1.0, sum = 1.0;
   bool ratio = false;
@@ -520,6 +522,7 @@ __device__ __forceinline__ void block_route(const BlockRoute& b, const SelectRul
     const double v = slot_x(k);
     gate[k] = (float)((ratio ? sel_sigmoid(v) / sm : exp(v - xm)) / sum * (double)r.scale);
   }
+  return true;
 }
 
 }  // namespace moe
