@@ -47,15 +47,6 @@ __device__ __forceinline__ void raise_abort(volatile int* abort, int* err) {
   atomicOr(err, ERR_GEMM_TIMEOUT);
 }
 
-// 32 bytes (a whole sector) in one store; p is 32-byte aligned.
-__device__ __forceinline__ void st32(void* p, const float* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p),
-               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
-               : "memory");
-}
-
 // ---------------------------------------------------------------- dE
 // A tile is 256 experts (128 rows of C per CTA of a pair) x a slab of 256
 // columns; its work is one unit for each 64 tokens.  The units of all tiles,
@@ -248,8 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* out = p.C + ((size_t)(pair + tile) * 256 + row) * BN + part * 64;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          st32(out + i * 16, &acc[i][0]);
-          st32(out + i * 16 + 8, &acc[i][8]);
+          st_global_v8(out + i * 16, &acc[i][0]);
+          st_global_v8(out + i * 16 + 8, &acc[i][8]);
         }
       }
       un = k1;

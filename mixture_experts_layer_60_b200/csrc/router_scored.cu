@@ -42,13 +42,14 @@ constexpr int BK = 64;                 // bf16 K elements per 128-byte swizzle r
 constexpr int TM = 128;                // token rows per CTA (TMEM lanes)
 constexpr int kMaxN = 256;
 constexpr int kChunk = 8;
-constexpr int STAGES = 6;
+constexpr int KW = 2;                 // blocks of 64 columns per stage
+constexpr int STAGES = 6 / KW;
 constexpr int kEpiWarps = 16;          // four per TMEM lane quarter, 16-column pieces in turn
 constexpr int kTcThreads = 64 + 32 * kEpiWarps;
 constexpr int kPieces = kMaxN / 16 / (kEpiWarps / 4);
 constexpr uint64_t kWaitNs = 1000000000ull;
-constexpr int A_BYTES = TM * BK * 2;
-constexpr int B_BYTES = (kMaxN / 2) * BK * 2;
+constexpr int A_BOX = TM * BK * 2, B_BOX = (kMaxN / 2) * BK * 2;
+constexpr int A_BYTES = KW * A_BOX, B_BYTES = KW * B_BOX;
 constexpr int OFF_B = STAGES * A_BYTES;
 constexpr int OFF_BAR = OFF_B + STAGES * B_BYTES;
 constexpr int N_BARS = 2 * STAGES + 5;           // full, empty, tfull[2], tempty[2], mma_done
@@ -127,21 +128,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      const uint32_t bytes = 2u * (uint32_t)(A_BYTES + (Nt / 2) * BK * 2);
+      const uint32_t bytes = 2u * (uint32_t)(A_BOX + (Nt / 2) * BK * 2);    // per block of 64
       for (int it = first; it < items && ok; it += step) {
         const int et = it % p.n_et, sl = (it / p.n_et) % p.S, tt = it / p.n_et / p.S;
         const int row0 = tt * 2 * TM + (int)half * TM, e0 = et * Nt + (int)half * (Nt / 2);
         const int kb1 = (sl + 1) * p.nk / p.S;
-        for (int kb = sl * p.nk / p.S; kb < kb1; ++kb) {
+        for (int kb = sl * p.nk / p.S; kb < kb1; kb += KW) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitNs)) {
             raise_abort(abort_flag, p.err);
             ok = false;
             break;
           }
-          if (is_leader) mbar_arrive_expect_tx(&full[stage], bytes);
+          const int n = min(KW, kb1 - kb);
+          if (is_leader) mbar_arrive_expect_tx(&full[stage], (uint32_t)n * bytes);
           const uint32_t fb = full_leader0 + stage * 8;
-          tma_load_2d_pair(sA + stage * A_BYTES, &tmU, kb * BK, row0, fb);
-          tma_load_2d_pair(sB + stage * B_BYTES, &tmE, kb * BK, e0, fb);
+          for (int i = 0; i < n; ++i) {
+            tma_load_2d_pair(sA + stage * A_BYTES + i * A_BOX, &tmU, (kb + i) * BK, row0, fb);
+            tma_load_2d_pair(sB + stage * B_BYTES + i * B_BOX, &tmE, (kb + i) * BK, e0, fb);
+          }
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
       }
@@ -168,19 +172,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           tc_fence_after();
           const int c1 = min(kb1, c0 + kChunk);
-          for (int kb = c0; kb < c1; ++kb) {
+          for (int kb = c0; kb < c1; kb += KW) {
             if (!mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitNs)) {
               raise_abort(abort_flag, p.err);
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t a0 = smem_u32(sA + stage * A_BYTES);
-            const uint32_t b0 = smem_u32(sB + stage * B_BYTES);
+            const int n = min(KW, c1 - kb);
+            for (int i = 0; i < n; ++i) {
+              const uint32_t a0 = smem_u32(sA + stage * A_BYTES + i * A_BOX);
+              const uint32_t b0 = smem_u32(sB + stage * B_BYTES + i * B_BOX);
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k)
-              mma2_f16_ss(tmem_base + buf * kMaxN, smem_desc_k_sw128(a0 + k * 32),
-                          smem_desc_k_sw128(b0 + k * 32), idesc, (kb > c0 || k > 0) ? 1u : 0u);
+              for (int k = 0; k < BK / 16; ++k)
+                mma2_f16_ss(tmem_base + buf * kMaxN, smem_desc_k_sw128(a0 + k * 32),
+                            smem_desc_k_sw128(b0 + k * 32), idesc,
+                            (kb > c0 || i > 0 || k > 0) ? 1u : 0u);
+            }
             mma2_commit_mask(&empty[stage], 3);
             if (++stage == STAGES) { stage = 0; phase ^= 1; }
           }
@@ -240,11 +248,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < kPieces; ++i) {
           const int piece = part + i * (kEpiWarps / 4);
           if (piece < n_pieces) {
-            float4* o = reinterpret_cast<float4*>(out + piece * 16);
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              o[v] = make_float4(acc[i][4 * v], acc[i][4 * v + 1], acc[i][4 * v + 2],
-                                 acc[i][4 * v + 3]);
+            st_global_v8(out + piece * 16, &acc[i][0]);
+            st_global_v8(out + piece * 16 + 8, &acc[i][8]);
           }
         }
       }
@@ -420,41 +425,42 @@ __global__ void __launch_bounds__(256) router_logits64_kernel(
 // A warp per token; the block's load histogram in shared memory, then added to
 // counts (whole numbers: the order of the additions does not matter).
 
-// The tokens listed for the exact pass: how many, and their ids; and those of
-// them whose every logit has to be exact: how many, ids, finished shares and
+// The tokens listed for the exact pass: how many, their ids, and 32 words of
+// experts that the open decisions wait for (word l, bit j: expert j*32 + l);
+// and those of them whose every logit has to be exact: how many, ids, finished shares and
 // float64 logits [T][N_r].
 struct Recheck {
   int32_t* n;             // [2]
   int32_t* tok;
+  uint32_t* mask;
   int32_t* full_tok;
   int32_t* full_done;
   double* full_x;
 };
 
-// x[j]: the slices' sums, joined in float64 and rounded once; returns the
-// largest sum over slices of |partial| among this lane's experts.
+// x[j]: the slices' sums, joined in slice order; returns the largest sum over
+// slices of |partial| among this lane's experts.
 template <int V>
 __device__ __forceinline__ float join_slices(const float* __restrict__ row, int S, size_t stride,
                                              int N, float (&x)[V]) {
   const int lane = threadIdx.x & 31;
-  double a[V];
   float m[V], mag = 0.f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) { a[j] = 0.0; m[j] = 0.f; }
-  for (int s = 0; s < S; ++s) {
+  for (int j = 0; j < V; ++j) {
+    x[j] = j * 32 + lane < N ? row[j * 32 + lane] : 0.f;
+    m[j] = fabsf(x[j]);
+  }
+  for (int s = 1; s < S; ++s) {
+    row += stride;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int e = j * 32 + lane;
-      const float v = e < N ? row[s * stride + e] : 0.f;
-      a[j] += (double)v;
+      const float v = j * 32 + lane < N ? row[j * 32 + lane] : 0.f;
+      x[j] += v;
       m[j] += fabsf(v);
     }
   }
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    x[j] = (float)a[j];
-    mag = fmaxf(mag, m[j]);
-  }
+  for (int j = 0; j < V; ++j) mag = fmaxf(mag, m[j]);
   return mag;
 }
 
@@ -484,7 +490,17 @@ __global__ void __launch_bounds__(128) router_select_kernel(
     const TokenScale ts = select_keys<V>(x, bias, r, logit_err, sc, key);
     const Selection sel = select_core<V>(key, ts.err, r, wk, ti);
     if (sel.open) {
-      if (lane == 0) rc.tok[atomicAdd(rc.n, 1)] = t;
+      int slot = 0;
+      if (lane == 0) {
+        slot = atomicAdd(rc.n, 1);
+        rc.tok[slot] = t;
+      }
+      slot = __shfl_sync(0xffffffffu, slot, 0);
+      uint32_t mask = sel.mask;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (j * 32 + lane < N && takes_part(key[j], sel.lo, sel.hi, ts.err)) mask |= 1u << j;
+      rc.mask[(size_t)slot * 32 + lane] = mask;
       continue;                                     // its gates and load come with the exact pass
     }
     select_gates<V, float>(x, sel.e, ts.m, ts.z, r, ti, gate + (size_t)t * r.K);
@@ -511,6 +527,7 @@ __global__ void __launch_bounds__(MAXT) router_token_kernel(
     int32_t* __restrict__ counts, float* __restrict__ logits, Recheck rc, bool all_tokens) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ double part[MAXT / 32][kDots];
+  __shared__ int n_want;
   __shared__ double red[33];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = r.N_r, nv = d / 8;
   const BlockRoute b = block_route_smem(smem_raw, N, r.K);
@@ -519,27 +536,33 @@ __global__ void __launch_bounds__(MAXT) router_token_kernel(
   const int n = all_tokens ? T : rc.n[0];
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int t = all_tokens ? i : rc.tok[i];
-    double a = 0.0, mag = 0.0;
+    double a = 0.0;
+    float mag = 0.f;
     if (tid < N) {
       const size_t at = (size_t)t * ld + tid, stride = (size_t)T * ld;
-      for (int s = 0; s < S; ++s) {
-        const double v = EXACT ? static_cast<const double*>(P)[at + s * stride]
-                               : (double)static_cast<const float*>(P)[at + s * stride];
-        a += v;
-        mag += fabs(v);
+      if (EXACT) {
+        for (int s = 0; s < S; ++s) a += static_cast<const double*>(P)[at + s * stride];
+      } else {
+        // as the first pass joined them
+        float f = static_cast<const float*>(P)[at];
+        mag = fabsf(f);
+        for (int s = 1; s < S; ++s) {
+          const float v = static_cast<const float*>(P)[at + s * stride];
+          f += v;
+          mag += fabsf(v);
+        }
+        a = (double)f;
       }
-      // float32 slices: the logit rounded once, as the first pass saw it
-      if (!EXACT) a = (double)(float)a;
       if (logits) logits[(size_t)t * N + tid] = (float)a;
     }
     float logit_err = 0.f;
     if (!EXACT) {
-      mag = block_reduce(mag, false, red);
-      logit_err = mag == 0.0 ? 0.f : kLogitError * fmaxf(4.f, (float)mag);
+      mag = (float)block_reduce((double)mag, false, red);
+      logit_err = mag == 0.f ? 0.f : kLogitError * fmaxf(4.f, mag);
     }
     if (tid < N) {
       b.x[tid] = a;
-      b.exact_f[tid] = EXACT || mag == 0.0;
+      b.exact_f[tid] = EXACT || mag == 0.f;
     }
     const auto fetch = [&](int nl) {
       const uint4* ur = reinterpret_cast<const uint4*>(u + (size_t)t * d);
@@ -583,6 +606,16 @@ __global__ void __launch_bounds__(MAXT) router_token_kernel(
         __syncthreads();
       }
     };
+    if (!EXACT && !all_tokens && mag != 0.f) {
+      // the experts that the first pass found wanting
+      if (tid == 0) n_want = 0;
+      __syncthreads();
+      const bool want = tid < N && ((rc.mask[(size_t)i * 32 + lane] >> warp) & 1u);
+      if (want) b.list[atomicAdd(&n_want, 1)] = (uint16_t)tid;
+      __syncthreads();
+      fetch(n_want);
+      if (want) b.exact_f[tid] = 1;
+    }
     const bool done = block_route(b, r, bias, logit_err, fetch, idx + (size_t)t * r.K,
                                   gate + (size_t)t * r.K, counts);
     if (!done && tid == 0) {
@@ -682,11 +715,12 @@ size_t tc_ws_bytes(int T, int d, int N, Recheck* rc, uint8_t* base) {
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes, 256); return at; };
   take((size_t)L.S * T * L.ld * 4);
-  const size_t n = take(8), tok = take((size_t)T * 4), ftok = take((size_t)T * 4),
+  const size_t n = take(8), tok = take((size_t)T * 4), mask = take((size_t)T * 128), ftok = take((size_t)T * 4),
                fdone = take((size_t)T * 4), fx = take((size_t)T * N * 8);
   if (rc) {
     rc->n = reinterpret_cast<int32_t*>(base + n);
     rc->tok = reinterpret_cast<int32_t*>(base + tok);
+    rc->mask = reinterpret_cast<uint32_t*>(base + mask);
     rc->full_tok = reinterpret_cast<int32_t*>(base + ftok);
     rc->full_done = reinterpret_cast<int32_t*>(base + fdone);
     rc->full_x = reinterpret_cast<double*>(base + fx);

@@ -145,11 +145,21 @@ __device__ __forceinline__ TokenScale select_keys(const float (&x)[V], const flo
 }
 
 // What a warp's selection decided: lane k's expert of slot k (k < 32; every
-// slot is in idx), and whether a decision is open.
+// slot is in idx), whether a decision is open, the keys between which the
+// open decisions of the order lie (none: lo > hi), and this lane's experts
+// (bit j) that an open choice of groups waits for.
 struct Selection {
   int e;
   bool open;
+  float lo, hi;
+  uint32_t mask;
 };
+
+// Whether an expert with this key can take part in the open decisions.
+__device__ __forceinline__ bool takes_part(float key, float lo, float hi, float err) {
+  const float pad = 3.f * err + 2.f * kKeyRounding * fabsf(key);
+  return key >= lo - pad && key <= hi + pad;
+}
 
 // key: this lane's keys, off by at most err + kKeyRounding |key| (err == 0:
 // exact).  wk: N_r floats of shared memory for this warp.
@@ -159,7 +169,7 @@ __device__ __forceinline__ Selection select_core(const float (&key)[V], float er
                                                  int32_t* __restrict__ idx) {
   const int lane = threadIdx.x & 31, N = r.N_r;
   const float rel = err > 0.f ? kKeyRounding : 0.f;
-  Selection out{0, false};
+  Selection out{0, false, INFINITY, -INFINITY, 0u};
   uint32_t ko[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) ko[j] = j * 32 + lane < N ? sel_ord(key[j]) : 0u;
@@ -211,18 +221,31 @@ __device__ __forceinline__ Selection select_core(const float (&key)[V], float er
     uint32_t go = 0u;
     if (lane < r.n_groups) go = sel_ord(two ? sel_val(ga) + sel_val(gb) : sel_val(ga));
     unsigned kept = 0;
-    float last = INFINITY;
+    float last = INFINITY, next = 0.f;
+    const float gsc = lane < r.n_groups ? sel_val(go) : NAN;
     for (int k = 0; k <= r.topk_groups; ++k) {       // one more round: the best group left out
       const uint32_t mx = __reduce_max_sync(0xffffffffu, go);
       if (mx == 0u) break;
       const int bg = __ffs(__ballot_sync(0xffffffffu, go == mx)) - 1;
-      const float v = sel_val(mx);
+      next = sel_val(mx);
       if (k < r.topk_groups) {
         kept |= 1u << bg;
-        last = v;
+        last = next;
         if (lane == bg) go = 0u;
       } else {
-        out.open = last - v < 2.f * r.group_top * err + rel * (fabsf(last) + fabsf(v));
+        out.open = last - next < 2.f * r.group_top * err + rel * (fabsf(last) + fabsf(next));
+      }
+    }
+    if (out.open) {
+      // the members that can enter the scores of the groups near the border
+      const float room = 4.f * r.group_top * err + 2.f * rel * (fabsf(last) + fabsf(next));
+      const float need = gsc >= next - room && gsc <= last + room ? sel_val(two ? gb : ga) : INFINITY;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const uint32_t e = j * 32 + lane, g = e < (uint32_t)N ? e * inv_gs >> 22 : 0u;
+        const float want = __shfl_sync(0xffffffffu, need, g);
+        if (e < (uint32_t)N && key[j] >= want - 2.f * err - 2.f * rel * fabsf(want))
+          out.mask |= 1u << j;
       }
     }
 #pragma unroll
@@ -244,7 +267,11 @@ __device__ __forceinline__ Selection select_core(const float (&key)[V], float er
     if (mx == 0u) break;                             // nothing eligible is left
     const int be = __reduce_min_sync(0xffffffffu, lb == mx ? lj * 32 + lane : 0x7fffffff);
     const float v = sel_val(mx);
-    if (prev - v < 2.f * err + rel * (fabsf(prev) + fabsf(v))) out.open = true;
+    if (prev - v < 2.f * err + rel * (fabsf(prev) + fabsf(v))) {
+      out.open = true;
+      out.lo = fminf(out.lo, v);
+      out.hi = fmaxf(out.hi, prev);
+    }
     prev = v;
     if (k == r.K) break;
 #pragma unroll
@@ -478,9 +505,7 @@ __device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRul
       }
       if (__syncthreads_or(z_open)) return false;
       if (s_hi >= 0 && mine && !ex) {
-        const float lo = b.top_key[s_hi], hi = b.top_key[s_lo - 1];
-        const float pad = 3.f * err + 2.f * rel * fabsf(key);
-        want = want || (key >= lo - pad && key <= hi + pad);
+        want = want || takes_part(key, b.top_key[s_hi], b.top_key[s_lo - 1], err);
       }
       open = __syncthreads_or(want);
     }
