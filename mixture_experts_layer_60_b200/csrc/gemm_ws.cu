@@ -70,7 +70,8 @@ constexpr int OFF_AMAX = OFF_TAB + 2 * (kMaxGroups + 1) * 4;
 // and a barrier for each (half, slot)
 constexpr int AMAX_BYTES = 2 * 2 * 4 * 2 * 32 * 4;
 constexpr int OFF_XBAR = (OFF_AMAX + AMAX_BYTES + 7) / 8 * 8;
-constexpr int SMEM_BYTES = OFF_XBAR + 4 * 8;
+constexpr int OFF_TMAX = OFF_XBAR + 4 * 8;
+constexpr int SMEM_BYTES = OFF_TMAX + 8;
 constexpr int SMEM_ALLOC = SMEM_BYTES + 1024;
 
 struct WsParams {
@@ -98,16 +99,16 @@ template <int EPI>
 struct TileMath {
   static constexpr bool SW =
       EPI == WS_SWIGLU || EPI == WS_SWIGLU_SAVE || EPI == WS_SWIGLU_SAVE8;
-  static constexpr bool DSW = EPI == WS_DSWIGLU || EPI == WS_DSWIGLU8;
+  static constexpr bool CHECK8 = EPI == WS_SWIGLU_SAVE8 || EPI == WS_DSWIGLU8;
   static constexpr int OUT_COLS = SW ? 128 : 256;   // output columns per weight tile
 };
 
 // Token tiling of a group of m rows: tiles of `step` rows (a multiple of 16,
-// at most 256, about m / ceil(m/256)); n_t = ceil(m / step) tiles, each with
+// at most tmax, about m / ceil(m/tmax)); n_t = ceil(m / step) tiles, each with
 // at least one row, the last one possibly shorter.
-__device__ __forceinline__ void token_tiling(int m, int& n_t, int& step) {
+__device__ __forceinline__ void token_tiling(int m, int& n_t, int& step, int tmax) {
   if (m <= 0) { n_t = 0; step = 16; return; }
-  const int n0 = (m + TMAX - 1) / TMAX;
+  const int n0 = (m + tmax - 1) / tmax;
   step = ((m + n0 - 1) / n0 + 15) / 16 * 16;
   n_t = (m + step - 1) / step;
 }
@@ -128,7 +129,7 @@ __device__ __forceinline__ void group_span(int g, int G, const int* roff, const 
 // Tile t -> group g, weight tile nt, first C row tok0, rows count, and the
 // first row xrow0 of X that the tile reads.
 __device__ __forceinline__ void decode_tile(int t, const int* prefix, const int* roff, int G,
-                                            int Gtot, const WsParams& p, int& g, int& nt,
+                                            int Gtot, const WsParams& p, int tmax, int& g, int& nt,
                                             int& tok0, int& count, int& xrow0) {
   int lo = 0, hi = Gtot - 1;
   while (lo < hi) {
@@ -139,7 +140,7 @@ __device__ __forceinline__ void decode_tile(int t, const int* prefix, const int*
   int base, m;
   group_span(g, G, roff, p, base, m);
   int n_t, step;
-  token_tiling(m, n_t, step);
+  token_tiling(m, n_t, step, tmax);
   const int local = t - prefix[g];
   nt = local / n_t;
   const int ti = local - nt * n_t;
@@ -170,6 +171,35 @@ __device__ __forceinline__ void e4m3x8(const uint2& v, float sc, float* f) {
   }
 }
 
+// v / sc rounded to nearest, from r = 1 / sc (rounded to nearest): the quotient
+// v r corrected by its remainder (Markstein's division; exact while nothing
+// leaves the normal range, which the caller checks by sc).
+__device__ __forceinline__ float div_by(float v, float sc, float r) {
+  const float q = v * r;
+  return fmaf(fmaf(-q, sc, v), r, q);
+}
+
+// What DSWIGLU8 reads of one 32-token chunk, in eight pieces of 8 columns of a
+// row: gate and up codes and their scales.  Piece i: column half i / 4, token
+// half i / 2 % 2, rows i % 2 * 8 + lane / 4.
+struct CheckpointPieces {
+  uint2 a[8], b[8];
+  float sa[8], sb[8];
+  __device__ __forceinline__ void read(const WsParams& p, int i, int c, int lane, int q, int nt,
+                                       int tok0, int count) {
+    const int tok = c * 32 + (i >> 1 & 1) * 16 + (i & 1) * 8 + (lane >> 2);
+    if (tok >= count || !in_bounds(tok0 + tok < p.rows, p.err)) return;
+    const size_t row = (size_t)(tok0 + tok);
+    const int col = nt * 256 + (i >> 2) * 128 + q * 32 + (lane & 3) * 8;
+    const uint8_t* qp = p.Q + row * p.lds + col;
+    const float* sp = p.QS + row * (p.lds / 128) + col / 128;
+    a[i] = *reinterpret_cast<const uint2*>(qp);
+    b[i] = *reinterpret_cast<const uint2*>(qp + p.N);
+    sa[i] = sp[0];
+    sb[i] = sp[p.N / 128];
+  }
+};
+
 // SiLU for a bf16 result: fast exponential and division are well inside bf16 rounding.
 __device__ __forceinline__ float silu_f(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
 
@@ -199,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
   float* amax_x = reinterpret_cast<float*>(smem + OFF_AMAX);
   uint64_t* xbar = reinterpret_cast<uint64_t*>(smem + OFF_XBAR);
+  int* s_tmax = reinterpret_cast<int*>(smem + OFF_TMAX);
   int* prefix = reinterpret_cast<int*>(smem + OFF_TAB);
   int* roff = prefix + kMaxGroups + 1;
 
@@ -237,13 +268,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     load_offsets_warp(p.offsets, G, p.rows, roff, p.err);
     const int per = (Gtot + 31) / 32;
     const int g0 = lane * per;
+    int tmax = TMAX;
+    if (TileMath<EPI>::CHECK8) {
+      // The tokens per tile that finish first: rounds of the grid times the
+      // cycles of a tile, which are the larger of its products (4 n a K step
+      // of 64) and of its operands through L2 (512 + 2 n), and an epilogue
+      // that nothing overlaps.  152 tiles of 256 on 148 SMs take two rounds;
+      // smaller tiles cost more per token but waste no second round.
+      long long best = -1;
+      for (int n = TMAX; n >= 64; n -= 32) {
+        int tiles = 0;
+        for (int i = 0; i < per; ++i)
+          if (g0 + i < Gtot) {
+            int base, m, n_t, step;
+            group_span(g0 + i, G, roff, p, base, m);
+            token_tiling(m, n_t, step, n);
+            tiles += n_t * n_wt;
+          }
+        tiles = __reduce_add_sync(0xffffffffu, tiles);
+        const long long rounds = (tiles + gridDim.x - 1) / gridDim.x;
+        const long long cost = rounds * ((long long)(p.K / BK) * max(4 * n, 512 + 2 * n) + 48 * n);
+        if (best < 0 || cost < best) {
+          best = cost;
+          tmax = n;
+        }
+      }
+      if (lane == 0) *s_tmax = tmax;
+    }
     int local = 0;
     for (int i = 0; i < per; ++i) {
       const int g = g0 + i;
       if (g < Gtot) {
         int base, m, n_t, step;
         group_span(g, G, roff, p, base, m);
-        token_tiling(m, n_t, step);
+        token_tiling(m, n_t, step, tmax);
         local += n_t * n_wt;
       }
     }
@@ -261,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefix[g] = run;
         int base, m, n_t, step;
         group_span(g, G, roff, p, base, m);
-        token_tiling(m, n_t, step);
+        token_tiling(m, n_t, step, tmax);
         run += n_t * n_wt;
       }
     }
@@ -272,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int total = prefix[Gtot];
+  const int tmax = TileMath<EPI>::CHECK8 ? *s_tmax : TMAX;
   const int nk = p.K / BK;
 
   if (warp == 0) {
@@ -282,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
         int g, nt, tok0, count, xrow0;
-        decode_tile(t, prefix, roff, G, Gtot, p, g, nt, tok0, count, xrow0);
+        decode_tile(t, prefix, roff, G, Gtot, p, tmax, g, nt, tok0, count, xrow0);
         const bool extra = g >= G;
         const CUtensorMap* tw = extra ? &tmW2 : &tmW;
         // one token box per stage: 64, 128 or 256 rows (it may read past the
@@ -327,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
         int g, nt, tok0, count, xrow0;
-        decode_tile(t, prefix, roff, G, Gtot, p, g, nt, tok0, count, xrow0);
+        decode_tile(t, prefix, roff, G, Gtot, p, tmax, g, nt, tok0, count, xrow0);
         const int n_mma = (count + 15) / 16 * 16;
         const uint32_t idesc = idesc_bf16_f32_major(128, n_mma, WMN, false);
         if (!mbar_wait_bounded(tempty, tphase ^ 1, abort_flag, kWaitNs)) {
@@ -375,7 +434,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool xok = true;
     for (int t = blockIdx.x; t < total && xok; t += gridDim.x) {
       int g, nt, tok0, count, xrow0;
-      decode_tile(t, prefix, roff, G, Gtot, p, g, nt, tok0, count, xrow0);
+      decode_tile(t, prefix, roff, G, Gtot, p, tmax, g, nt, tok0, count, xrow0);
+      CheckpointPieces ck;
+      if (EPI == WS_DSWIGLU8)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ck.read(p, i, ch, lane, q, nt, tok0, count);
       const bool got = mbar_wait_bounded(tfull, tphase, abort_flag, kWaitNs);
       if (!__all_sync(0xffffffffu, got)) {
         raise_abort(abort_flag, p.err);
@@ -384,7 +447,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t tl = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
       const int nch = (count + 31) / 32;
-      if (TileMath<EPI>::DSW) {
+      if constexpr (EPI == WS_DSWIGLU8) {
+        // dA from the checkpoint, and h again.  The pieces of a chunk were
+        // read ahead (under the products, or under the chunk before).
+        float* pf = reinterpret_cast<float*>(patch);
+        for (int c = ch; c < nch; c += 2) {
+          uint32_t r0[32], r1[32];
+          tmem_ld_32x32b_x32(tl + c * 32, r0);
+          tmem_ld_32x32b_x32(tl + 256 + c * 32, r1);
+          tmem_wait_ld();
+#pragma unroll
+          for (int hs = 0; hs < 4; ++hs) {
+            const int hh = hs >> 1, sub = hs & 1;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              pf[j * 32 + lane] = __uint_as_float(hh == 0 ? r0[sub * 16 + j] : r1[sub * 16 + j]);
+            __syncwarp();
+#pragma unroll
+            for (int it = 0; it < 2; ++it) {
+              const int piece = hs * 2 + it, row = it * 8 + (lane >> 2), c8 = (lane & 3) * 8;
+              const int tok = c * 32 + sub * 16 + row;
+              if (tok < count && in_bounds(tok0 + tok < p.rows, p.err)) {
+                const float4 d0 = *reinterpret_cast<const float4*>(pf + row * 32 + c8);
+                const float4 d1 = *reinterpret_cast<const float4*>(pf + row * 32 + c8 + 4);
+                const float dv[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+                float fa[8], fb[8], oa[8], ob[8], hv[8];
+                e4m3x8(ck.a[piece], ck.sa[piece], fa);
+                e4m3x8(ck.b[piece], ck.sb[piece], fb);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float sg = __fdividef(1.0f, 1.0f + __expf(-fa[i]));
+                  oa[i] = dv[i] * fb[i] * (sg * (1.0f + fa[i] * (1.0f - sg)));
+                  ob[i] = dv[i] * fa[i] * sg;
+                  hv[i] = fa[i] * sg * fb[i];
+                }
+                const size_t grow = (size_t)(tok0 + tok);
+                const int col = nt * 256 + hh * 128 + q * 32 + c8;
+                *reinterpret_cast<uint4*>(p.C + grow * p.ldc + col) = Vec<__nv_bfloat16>::store(oa);
+                *reinterpret_cast<uint4*>(p.C + grow * p.ldc + p.N + col) =
+                    Vec<__nv_bfloat16>::store(ob);
+                *reinterpret_cast<uint4*>(p.H + grow * p.N + col) = Vec<__nv_bfloat16>::store(hv);
+              }
+              ck.read(p, piece, c + 2, lane, q, nt, tok0, count);
+            }
+            __syncwarp();
+          }
+        }
+      } else if constexpr (EPI == WS_DSWIGLU) {
         // dh[tok, col] from TMEM; a = S[tok, col], b = S[tok, I + col]:
         //   dA[tok, col] = dh * b * SiLU'(a),  dA[tok, I + col] = dh * SiLU(a).
         // dh goes through a float32 [16 tok][32 col] patch so that every
@@ -405,8 +514,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
               // both 16-byte pieces of this lane first, then the arithmetic
               uint4 av[2], bv[2];
-              uint2 aq[2], bq[2];
-              float as[2], bs[2];
               size_t grow[2];
               int col[2], c8[2], row[2];
               bool ok[2];
@@ -421,17 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 grow[it] = (size_t)(tok0 + (ok[it] ? tok : 0));
                 col[it] = nt * 256 + hh * 128 + q * 32 + c8[it];
                 if (ok[it]) {
-                  if (EPI == WS_DSWIGLU8) {
-                    const uint8_t* qp = p.Q + grow[it] * p.lds + col[it];
-                    const float* sp = p.QS + grow[it] * (p.lds / 128) + col[it] / 128;
-                    aq[it] = *reinterpret_cast<const uint2*>(qp);
-                    bq[it] = *reinterpret_cast<const uint2*>(qp + p.N);
-                    as[it] = sp[0];
-                    bs[it] = sp[p.N / 128];
-                  } else {
-                    av[it] = *reinterpret_cast<const uint4*>(p.S + grow[it] * p.lds + col[it]);
-                    bv[it] = *reinterpret_cast<const uint4*>(p.S + grow[it] * p.lds + p.N + col[it]);
-                  }
+                  av[it] = *reinterpret_cast<const uint4*>(p.S + grow[it] * p.lds + col[it]);
+                  bv[it] = *reinterpret_cast<const uint4*>(p.S + grow[it] * p.lds + p.N + col[it]);
                 }
               }
 #pragma unroll
@@ -441,24 +539,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const float4 d1 = *reinterpret_cast<const float4*>(pf + row[it] * 32 + c8[it] + 4);
                   const float dv[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
                   float fa[8], fb[8], oa[8], ob[8];
-                  float hv[8];
-                  if (EPI == WS_DSWIGLU8) {
-                    e4m3x8(aq[it], as[it], fa);
-                    e4m3x8(bq[it], bs[it], fb);
-                  } else {
-                    Vec<__nv_bfloat16>::load(av[it], fa);
-                    Vec<__nv_bfloat16>::load(bv[it], fb);
-                  }
+                  Vec<__nv_bfloat16>::load(av[it], fa);
+                  Vec<__nv_bfloat16>::load(bv[it], fb);
 #pragma unroll
                   for (int i = 0; i < 8; ++i) {
                     const float sg = __fdividef(1.0f, 1.0f + __expf(-fa[i]));
                     oa[i] = dv[i] * fb[i] * (sg * (1.0f + fa[i] * (1.0f - sg)));
                     ob[i] = dv[i] * fa[i] * sg;
-                    if (EPI == WS_DSWIGLU8) hv[i] = fa[i] * sg * fb[i];
                   }
-                  if (EPI == WS_DSWIGLU8)
-                    *reinterpret_cast<uint4*>(p.H + grow[it] * p.N + col[it]) =
-                        Vec<__nv_bfloat16>::store(hv);
                   *reinterpret_cast<uint4*>(p.C + grow[it] * p.ldc + col[it]) =
                       Vec<__nv_bfloat16>::store(oa);
                   *reinterpret_cast<uint4*>(p.C + grow[it] * p.ldc + p.N + col[it]) =
@@ -536,14 +624,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             mu = fmaxf(mu, slot[o * 64 + 32 + lane]);
           }
           const float sg = amax_scale(mg), su = amax_scale(mu);
+          // lanes hold the scales and reciprocals of token c*32 + lane; scales
+          // too small for div_by's remainder divide plainly
+          const float rg = __frcp_rn(sg), ru = __frcp_rn(su);
+          const bool plain = __any_sync(0xffffffffu, fminf(sg, su) < 1e-30f || fmaxf(mg, mu) > 1e30f);
           uint8_t* pb = reinterpret_cast<uint8_t*>(patch);       // [32 tok][32 col]
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const float sc = __shfl_sync(0xffffffffu, hh ? su : sg, j);
+              const float rc = __shfl_sync(0xffffffffu, hh ? ru : rg, j);
+              const float v = __uint_as_float(hh ? r1[j] : r0[j]);
               pb[j * 32 + lane] = static_cast<uint8_t>(__nv_cvt_float_to_fp8(
-                  __fdiv_rn(__uint_as_float(hh ? r1[j] : r0[j]), sc), __NV_SATFINITE, __NV_E4M3));
+                  plain ? __fdiv_rn(v, sc) : div_by(v, sc, rc), __NV_SATFINITE, __NV_E4M3));
             }
             __syncwarp();
             const int colq = (hh ? p.N : 0) + nt * 128 + q * 32;
@@ -654,8 +748,10 @@ moe_status ws_launch(const void* X, const void* W, int b_rows_per_group, const i
   p.x_extra_local = ex.x_local ? 1 : 0;
   p.err = device_error_word();
   if (!p.err) return fail(MOE_ERR_CUDA, "device error word unavailable");
+  // the 8-bit checkpoint epilogues may take tiles of down to 64 tokens
+  const int tile = TileMath<EPI>::CHECK8 ? 64 : TMAX;
   const long long max_tiles =
-      ((long long)(rows + TMAX - 1) / TMAX + (offsets ? G : 0) +
+      ((long long)(rows + tile - 1) / tile + (offsets ? G : 0) +
        (long long)ex.n_extra * ((ex.T + TMAX - 1) / TMAX)) * (N / OUT_COLS);
   int grid = sm_count();
   if (max_tiles < grid) grid = (int)(max_tiles > 0 ? max_tiles : 1);
