@@ -985,10 +985,10 @@ moe_status moe_expert_ffn_backward8(const void* x, const int32_t* offsets, int n
   void* tail = static_cast<uint8_t*>(h) + align_up((size_t)rows * I * 2, 256);
   // Dgrad of the down projection fused with the SwiGLU backward -> dA, h
   MOE_TRY(launch_ws_dswiglu8(dy, W_down, offsets, n_groups, rows, I, d, a_q, a_scale, dA, h, s));
-  MOE_TRY(launch_wgrad_gemm(dy, d, h, I, offsets, n_groups, rows, tail, dW_down, s));
+  MOE_TRY(launch_wgrad_gemm(dy, d, h, I, offsets, n_groups, rows, tail, dW_down, s, true));
   MOE_TRY(launch_ws_gemm_ex(dA, W_gate_up, 0, offsets, n_groups, rows, d, 2 * I, WS_STORE, true,
-                            dx, d, nullptr, 0, s));
-  return launch_wgrad_gemm(dA, 2 * I, x, d, offsets, n_groups, rows, tail, dW_gate_up, s);
+                            dx, d, nullptr, 0, s, nullptr, true));
+  return launch_wgrad_gemm(dA, 2 * I, x, d, offsets, n_groups, rows, tail, dW_gate_up, s, true);
 }
 
 // ---------------------------------------------------------------- expert parallelism

@@ -173,7 +173,7 @@ __device__ __forceinline__ void e4m3x8(const uint2& v, float sc, float* f) {
 
 // v / sc rounded to nearest, from r = 1 / sc (rounded to nearest): the quotient
 // v r corrected by its remainder (Markstein's division; exact while nothing
-// leaves the normal range, which the caller checks by sc).
+// leaves the normal range, which the caller sees to).
 __device__ __forceinline__ float div_by(float v, float sc, float r) {
   const float q = v * r;
   return fmaf(fmaf(-q, sc, v), r, q);
@@ -328,6 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();                  // launched with `after`: the setup overlaps the kernel before
+  pdl_trigger();
   const uint32_t tmem_base = *tmem_slot;
   const int total = prefix[Gtot];
   const int tmax = TileMath<EPI>::CHECK8 ? *s_tmax : TMAX;
@@ -624,20 +626,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             mu = fmaxf(mu, slot[o * 64 + 32 + lane]);
           }
           const float sg = amax_scale(mg), su = amax_scale(mu);
-          // lanes hold the scales and reciprocals of token c*32 + lane; scales
-          // too small for div_by's remainder divide plainly
-          const float rg = __frcp_rn(sg), ru = __frcp_rn(su);
-          const bool plain = __any_sync(0xffffffffu, fminf(sg, su) < 1e-30f || fmaxf(mg, mu) > 1e30f);
+          // token c*32 + lane: its two scales, their reciprocals and a power of
+          // two that brings values and scale into div_by's range (the quotient
+          // is the same; an infinite scale divides finite values to 0), for
+          // every lane of the warp to read back
           uint8_t* pb = reinterpret_cast<uint8_t*>(patch);       // [32 tok][32 col]
+          float4* ps = reinterpret_cast<float4*>(pb + 1024);     // [gate, up][32 tok]
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const float sc = hh ? su : sg;
+            const float f = sc < 1e-30f ? 0x1p64f : sc > 1e27f ? 0x1p-64f : 1.f;
+            const bool inf = sc > 3e38f;
+            ps[hh * 32 + lane] = make_float4(inf ? 0.f : sc * f, inf ? 0.f : __frcp_rn(sc * f), f, 0.f);
+          }
+          __syncwarp();
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const float sc = __shfl_sync(0xffffffffu, hh ? su : sg, j);
-              const float rc = __shfl_sync(0xffffffffu, hh ? ru : rg, j);
-              const float v = __uint_as_float(hh ? r1[j] : r0[j]);
-              pb[j * 32 + lane] = static_cast<uint8_t>(__nv_cvt_float_to_fp8(
-                  plain ? __fdiv_rn(v, sc) : div_by(v, sc, rc), __NV_SATFINITE, __NV_E4M3));
+              const float4 d = ps[hh * 32 + j];
+              const float v = __uint_as_float(hh ? r1[j] : r0[j]) * d.z;
+              pb[j * 32 + lane] = static_cast<uint8_t>(
+                  __nv_cvt_float_to_fp8(div_by(v, d.x, d.y), __NV_SATFINITE, __NV_E4M3));
             }
             __syncwarp();
             const int colq = (hh ? p.N : 0) + nt * 128 + q * 32;
@@ -688,7 +698,7 @@ template <int EPI, bool WMN>
 moe_status ws_launch(const void* X, const void* W, int b_rows_per_group, const int32_t* offsets,
                      int n_groups, int rows, int N, int K, void* C, int ldc, void* S, int lds,
                      const WsExtraGroups& ex, cudaStream_t s, uint8_t* Q = nullptr,
-                     float* QS = nullptr, void* H = nullptr) {
+                     float* QS = nullptr, void* H = nullptr, bool after = false) {
   constexpr int OUT_COLS = TileMath<EPI>::OUT_COLS;
   CUtensorMap tmW, tmX, tmX128, tmX256, tmW2, tmX2, tmX2_128, tmX2_256;
   const int G = offsets ? n_groups : 1;
@@ -755,6 +765,9 @@ moe_status ws_launch(const void* X, const void* W, int b_rows_per_group, const i
        (long long)ex.n_extra * ((ex.T + TMAX - 1) / TMAX)) * (N / OUT_COLS);
   int grid = sm_count();
   if (max_tiles < grid) grid = (int)(max_tiles > 0 ? max_tiles : 1);
+  if (after)
+    return launch_after(kern, dim3(grid), dim3(kThreads), SMEM_ALLOC, s, 1, "ws_gemm launch", tmW, tmX,
+                        tmX128, tmX256, tmW2, tmX2, tmX2_128, tmX2_256, p);
   kern<<<grid, kThreads, SMEM_ALLOC, s>>>(tmW, tmX, tmX128, tmX256, tmW2, tmX2, tmX2_128, tmX2_256, p);
   return cuda_check(cudaGetLastError(), "ws_gemm launch");
 }
@@ -774,7 +787,7 @@ moe_status launch_ws_gemm(const void* X, const void* W, int b_rows_per_group,
 moe_status launch_ws_gemm_ex(const void* X, const void* W, int b_rows_per_group,
                              const int32_t* offsets, int n_groups, int rows, int N, int K,
                              WsEpi epi, bool w_mn, void* C, int ldc, void* S, int lds,
-                             cudaStream_t s, const WsExtraGroups* extra) {
+                             cudaStream_t s, const WsExtraGroups* extra, bool after) {
   const WsExtraGroups none{};
   const WsExtraGroups& ex = extra ? *extra : none;
   if (ex.n_extra && (epi == WS_SWIGLU_SAVE || epi == WS_DSWIGLU || w_mn))
@@ -796,7 +809,8 @@ moe_status launch_ws_gemm_ex(const void* X, const void* W, int b_rows_per_group,
                                               N, K, C, ldc, S, lds, ex, s);
     case WS_STORE:
       return w_mn ? ws_launch<WS_STORE, true>(X, W, b_rows_per_group, offsets, n_groups, rows, N,
-                                              K, C, ldc, S, lds, ex, s)
+                                              K, C, ldc, S, lds, ex, s, nullptr, nullptr, nullptr,
+                                              after)
                   : ws_launch<WS_STORE, false>(X, W, b_rows_per_group, offsets, n_groups, rows,
                                                N, K, C, ldc, S, lds, ex, s);
     case WS_DSWIGLU:

@@ -123,12 +123,15 @@ moe_status launch_ws2_gemm(const void* X, const void* W, int b_rows_per_group,
 //            DSWIGLU dh = the product (N = I columns), a = S[:, 0:I], b = S[:, I:2I]:
 //                    C[:, 0:I] = dh * b * SiLU'(a), C[:, I:2I] = dh * SiLU(a).
 // w_mn: W is stored [G*K rows][N cols] (N contiguous) instead of [G*rows_per_group][K].
+// after (WS_STORE with w_mn; the weight gradients below too): launched over the
+// tail of the stream's previous kernel (launch_after).
 enum WsEpi { WS_SWIGLU = 0, WS_STORE = 1, WS_SWIGLU_SAVE = 2, WS_DSWIGLU = 3,
              WS_SWIGLU_SAVE8 = 4, WS_DSWIGLU8 = 5 };   // the 8s: by their own launchers below
 moe_status launch_ws_gemm_ex(const void* X, const void* W, int b_rows_per_group,
                              const int32_t* offsets, int n_groups, int rows, int N, int K,
                              WsEpi epi, bool w_mn, void* C, int ldc, void* S, int lds,
-                             cudaStream_t s, const WsExtraGroups* extra = nullptr);
+                             cudaStream_t s, const WsExtraGroups* extra = nullptr,
+                             bool after = false);
 
 // SWIGLU_SAVE8  h [rows, I] bf16, and the float32 gate and up pre-activations as E4M3 a_q
 //               [rows, 2I] with a_scale [rows, 2I/128] (amax/448 per row and 128 columns)
@@ -163,11 +166,12 @@ moe_status launch_gather_pipe(int mode, moe_dtype dt, const void* a, const void*
 // A_tail: scratch of wgrad_tail_bytes(M * 2, 64, groups) bytes for the groups'
 // zero-padded last 64-row blocks of A.
 moe_status launch_wgrad_gemm(const void* A, int M, const void* B, int N, const int32_t* offsets,
-                             int n_groups, int rows, void* A_tail, void* C, cudaStream_t s);
+                             int n_groups, int rows, void* A_tail, void* C, cudaStream_t s,
+                             bool after = false);
 // T[g] = the last block_rows-row block of group g of A (rows past the group zeroed).
 moe_status launch_wgrad_tails(const void* A, size_t row_bytes, int block_rows,
                               const int32_t* offsets, int n_groups, int rows, void* T,
-                              cudaStream_t s);
+                              cudaStream_t s, bool after = false);
 size_t wgrad_tail_bytes(size_t row_bytes, int block_rows, int n_groups);
 
 // gemm_wgrad_fp8.cu ----------------------------------------------------------
