@@ -373,52 +373,85 @@ __global__ void __launch_bounds__(128) router_logits_few_kernel(
 constexpr int kFewTokens = 8;
 
 // ---------------------------------------------------------------- float64 logits
-// P[s][t][i] = sum over slice s of d of u[t,k] E[i,k], float64 products and
-// sums.  A 32-token x 32-expert tile per block of 256 threads (2 x 2 outputs a
-// thread), 32 columns of both operands staged in shared memory as float64.
-// Bound by the float64 rate (64 FMA per SM and cycle) and shared memory.
-constexpr int kT64 = 32;
+// P[s][t][i] = sum over slice s of d of u[t,k] E[i,k] of float32 inputs, on the
+// float64 tensor pipe (m8n8k4).  A 32-token x 64-expert tile per block of four
+// warps (16 x 32 each, eight products per four columns for six operand loads;
+// one output per thread from shared memory was bound by those loads, 53 us at
+// T 1037, d 2048, N_r 61), 32 columns of both operands staged as float64 while
+// the next 32 are on their way.  Bound by the float64 rate.
+constexpr int kT64 = 32, kE64 = 64, kK64 = 32, kLd64 = kK64 + 4;
 
-template <typename Tin>
-__global__ void __launch_bounds__(256) router_logits64_kernel(
-    const Tin* __restrict__ u, const Tin* __restrict__ E, int T, int d, int N, int S, int ld,
+__device__ __forceinline__ void mma_f64(double& c0, double& c1, double a, double b) {
+  asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0,%1}, {%2}, {%3}, {%0,%1};"
+               : "+d"(c0), "+d"(c1)
+               : "d"(a), "d"(b));
+}
+
+__global__ void __launch_bounds__(128) router_logits64_kernel(
+    const float* __restrict__ u, const float* __restrict__ E, int T, int d, int N, int S, int ld,
     double* __restrict__ P, int32_t* __restrict__ counts) {
-  __shared__ double su[kT64][kT64 + 1], se[kT64][kT64 + 1];
-  const int tid = threadIdx.x;
-  const int t0 = blockIdx.x * kT64, e0 = blockIdx.y * kT64, sl = blockIdx.z;
+  __shared__ double su[kT64][kLd64], se[kE64][kLd64];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int t0 = blockIdx.x * kT64, e0 = blockIdx.y * kE64, sl = blockIdx.z;
   pdl_trigger();
   if (blockIdx.x == 0 && blockIdx.y == 0 && sl == 0)
-    for (int i = tid; i < N; i += 256) counts[i] = 0;
-  const int nc = d / kT64;                                // d % 64 == 0
+    for (int i = tid; i < N; i += 128) counts[i] = 0;
+  const int nc = d / kK64;                                // d % 64 == 0
   const int c0 = (int)((long long)sl * nc / S), c1 = (int)((long long)(sl + 1) * nc / S);
-  const int tx = tid & 15, ty = tid >> 4;                 // experts tx, tx+16; tokens ty, ty+16
-  double a00 = 0, a01 = 0, a10 = 0, a11 = 0;
-  for (int c = c0; c < c1; ++c) {
-    for (int i = tid; i < kT64 * kT64; i += 256) {
-      const int r = i >> 5, k = i & 31;
-      su[r][k] = t0 + r < T ? (double)IO<Tin>::ld(u + (size_t)(t0 + r) * d + c * kT64 + k) : 0.0;
-      se[r][k] = e0 + r < N ? (double)IO<Tin>::ld(E + (size_t)(e0 + r) * d + c * kT64 + k) : 0.0;
+  // 96 rows of eight float4s: six a thread
+  constexpr int kLoads = (kT64 + kE64) * kK64 / 4 / 128;
+  float4 nx[kLoads];
+  const auto fetch = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = (i * 128 + tid) >> 3, k4 = (tid & 7) * 4 + c * kK64;
+      const bool is_u = r < kT64;
+      const int row = is_u ? t0 + r : e0 + r - kT64;
+      nx[i] = row < (is_u ? T : N)
+                  ? *reinterpret_cast<const float4*>((is_u ? u : E) + (size_t)row * d + k4)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    __syncthreads();
-#pragma unroll 8
-    for (int k = 0; k < kT64; ++k) {
-      const double x0 = su[ty][k], x1 = su[ty + 16][k], y0 = se[tx][k], y1 = se[tx + 16][k];
-      a00 = fma(x0, y0, a00);
-      a01 = fma(x0, y1, a01);
-      a10 = fma(x1, y0, a10);
-      a11 = fma(x1, y1, a11);
-    }
-    __syncthreads();
-  }
-  double* out = P + (size_t)sl * T * ld;
-  const double v[2][2] = {{a00, a01}, {a10, a11}};
+  };
+  double acc[2][4][2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int t = t0 + ty + 16 * i, e = e0 + tx + 16 * j;
-      if (t < T && e < N) out[(size_t)t * ld + e] = v[i][j];
+    for (int j = 0; j < 4; ++j) acc[i][j][0] = acc[i][j][1] = 0.0;
+  const int wt = (warp & 1) * 16 + (lane >> 2), we = (warp >> 1) * 32 + (lane >> 2), kk = lane & 3;
+  if (c0 < c1) fetch(c0);
+  for (int c = c0; c < c1; ++c) {
+    __syncthreads();                                      // the last columns have been used
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = (i * 128 + tid) >> 3, k4 = (tid & 7) * 4;
+      double* dst = r < kT64 ? &su[r][k4] : &se[r - kT64][k4];
+      dst[0] = nx[i].x; dst[1] = nx[i].y; dst[2] = nx[i].z; dst[3] = nx[i].w;
     }
+    __syncthreads();
+    if (c + 1 < c1) fetch(c + 1);
+#pragma unroll
+    for (int k = 0; k < kK64; k += 4) {
+      double a[2], b[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) a[i] = su[wt + 8 * i][k + kk];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = se[we + 8 * j][k + kk];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma_f64(acc[i][j][0], acc[i][j][1], a[i], b[j]);
+    }
+  }
+  double* out = P + (size_t)sl * T * ld;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = t0 + wt + 8 * i, e = e0 + (warp >> 1) * 32 + 8 * j + 2 * kk + h;
+        if (t < T && e < N) out[(size_t)t * ld + e] = acc[i][j][h];
+      }
 }
 
 // ---------------------------------------------------------------- selection
@@ -697,7 +730,7 @@ __global__ void __launch_bounds__(MAXT) router_full_kernel(
 // kMaxSlices64, each slice at least 128 columns.
 constexpr int kMaxSlices64 = 16;
 int slices64(int T, int d, int N) {
-  const long long tiles = (long long)((T + kT64 - 1) / kT64) * ((N + kT64 - 1) / kT64);
+  const long long tiles = (long long)((T + kT64 - 1) / kT64) * ((N + kE64 - 1) / kE64);
   long long S = (2LL * 148 + tiles - 1) / tiles;
   if (S > d / 128) S = d / 128;
   if (S > kMaxSlices64) S = kMaxSlices64;
@@ -856,10 +889,10 @@ moe_status launch_route_scored(const void* u, const void* E, moe_dtype dt, const
   int S = 1;
   if (dt == MOE_F32) {
     S = slices64(T, d, N_r);
-    const dim3 grid((T + kT64 - 1) / kT64, (N_r + kT64 - 1) / kT64, S);
-    router_logits64_kernel<float><<<grid, 256, 0, s>>>(static_cast<const float*>(u),
-                                                       static_cast<const float*>(E), T, d, N_r, S,
-                                                       N_r, P, counts);
+    const dim3 grid((T + kT64 - 1) / kT64, (N_r + kE64 - 1) / kE64, S);
+    router_logits64_kernel<<<grid, 128, 0, s>>>(static_cast<const float*>(u),
+                                                static_cast<const float*>(E), T, d, N_r, S, N_r, P,
+                                                counts);
   } else {
     const bf* ub = static_cast<const bf*>(u);
     const bf* eb = static_cast<const bf*>(E);
