@@ -27,6 +27,19 @@ class LayerConfig:
     outlier_scale: float = 1.0
     n_groups: int = 1        # > 1: expert groups for the per-token group (node) limit
     topk_groups: int = 1     # groups a token may use when n_groups > 1
+    # the router's choices (moe_route_scored; the defaults are moe_route's router)
+    score: str = "sigmoid"   # "sigmoid" | "softmax" over the routed experts
+    group_top: int = 1       # a group's score: the sum of its 1 or 2 largest keys
+    renorm: bool = True      # gates divided by the sum of the selected scores
+    gate_scale: float = 1.0  # gates multiplied by this
+    balance_alpha: float = 0.0   # > 0: sequence-wise balance loss in training steps
+    checkpoint8: bool = False    # bf16 training: activations kept in 8 bits (E4M3)
+
+    @property
+    def scored(self):
+        """Whether the layer routes with moe_route_scored."""
+        return (self.score != "sigmoid" or self.group_top != 1 or not self.renorm
+                or self.gate_scale != 1.0 or self.balance_alpha > 0)
 
     @property
     def R(self):

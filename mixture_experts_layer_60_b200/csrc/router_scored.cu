@@ -742,12 +742,26 @@ int dispatch_v(int N) {
   return V <= 1 ? 1 : V <= 2 ? 2 : V <= 4 ? 4 : V <= 8 ? 8 : V <= 16 ? 16 : 32;
 }
 
+// Rows of partial logits over every token count up to T: slices times tokens
+// is at most the larger of T and what fills the pairs once (so a workspace for
+// more tokens serves fewer).
+size_t slice_rows(int T, int n_et) {
+  const size_t fill = (size_t)kPairs * 2 * TM / n_et, most = (size_t)kMaxSlices * T;
+  const size_t rows = most < fill ? most : fill;
+  return rows > (size_t)T ? rows : (size_t)T;
+}
+size_t slice_rows64(int T, int N) {
+  const size_t et = (N + kE64 - 1) / kE64, most = (size_t)kMaxSlices64 * T;
+  const size_t fill = (size_t)T + (2 * 148 * kT64 + et - 1) / et + kT64;
+  return most < fill ? most : fill;
+}
+
 // Workspace of the tensor-core path: partial logits, then the listing.
 size_t tc_ws_bytes(int T, int d, int N, Recheck* rc, uint8_t* base) {
   const LogitTiling L = logit_tiling(T, d, N);
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes, 256); return at; };
-  take((size_t)L.S * T * L.ld * 4);
+  take(slice_rows(T, L.n_et) * L.ld * 4);
   const size_t n = take(8), tok = take((size_t)T * 4), mask = take((size_t)T * 128), ftok = take((size_t)T * 4),
                fdone = take((size_t)T * 4), fx = take((size_t)T * N * 8);
   if (rc) {
@@ -807,7 +821,7 @@ moe_status launch_logits_tc(const void* u, const void* E, int T, int d, int N, f
 size_t route_scored_ws_bytes(int T, int d, int N_r) {
   // the larger of the float64 and the tensor-core path's needs: the dtype is
   // not among the arguments
-  const size_t a = align_up((size_t)slices64(T, d, N_r) * T * N_r * sizeof(double), 256);
+  const size_t a = align_up(slice_rows64(T, N_r) * N_r * sizeof(double), 256);
   const size_t b = tc_ws_bytes(T, d, N_r, nullptr, nullptr);
   return a > b ? a : b;
 }

@@ -8,19 +8,29 @@ FP8 copies of them) and the per-step buffers, and runs one step as
        experts' moe_expert_ffn after them) -> moe_combine [-> moe_bias_update]
 on one CUDA stream.  For training (bf16 or FP8), forward_train keeps the
 activations the backward needs and backward(dh) returns du and fills
-self.grad with the gradients of E and of every expert weight.  Every step of the layer runs in libmoe's kernels; this
+self.grad with the gradients of E and of every expert weight.  A configuration
+whose router differs from moe_route's (softmax scores, group scores of two
+keys, raw or scaled gates, a balance loss) routes with moe_route_scored, and
+its backward ends in moe_route_scored_backward; checkpoint8 keeps the gate/up
+pre-activations in 8 bits between forward_train and backward.  Every step of the layer runs in libmoe's kernels; this
 module only allocates buffers and sequences calls.
 """
 from __future__ import annotations
 
 import torch
 
-from . import (MOE_BF16, MOE_E4M3, MOE_F32, moe_bias_update, moe_combine, moe_combine_backward,
+from . import (MOE_BF16, MOE_E4M3, MOE_F32, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX,
+               moe_balance_loss, moe_balance_loss_workspace_size, moe_bias_update, moe_combine,
+               moe_combine_backward,
                moe_expert_down, moe_expert_down_shared, moe_expert_ffn, moe_expert_ffn_backward,
                moe_expert_ffn_backward_workspace_size, moe_expert_ffn_workspace_size,
-               moe_expert_gate_up, moe_expert_gate_up_save, moe_expert_gate_up_shared, moe_permute,
+               moe_expert_ffn_backward8, moe_expert_ffn_backward8_workspace_size,
+               moe_expert_gate_up, moe_expert_gate_up_save, moe_expert_gate_up_save8,
+               moe_expert_gate_up_shared, moe_permute,
                moe_permute_workspace_size, moe_quantize_128x128, moe_quantize_1x128, moe_route,
-               moe_route_grouped, moe_route_workspace_size, moe_router_weight_grad,
+               moe_route_grouped, moe_route_scored, moe_route_scored_backward,
+               moe_route_scored_backward_workspace_size, moe_route_scored_workspace_size,
+               moe_route_workspace_size, moe_router_weight_grad,
                moe_unpermute_backward)
 from .configs import LayerConfig
 
@@ -39,6 +49,11 @@ class MoELayer:
         self.E = weights["E"]
         self.b = weights["b"].clone()
         self.fp8 = cfg.dtype == "e4m3"
+        if cfg.score not in ("sigmoid", "softmax"):
+            raise ValueError(f"unknown router score {cfg.score!r}")
+        if cfg.checkpoint8 and cfg.dtype != "bf16":
+            raise ValueError("8-bit activation checkpoints are implemented for bf16 layers")
+        self.score = MOE_SCORE_SOFTMAX if cfg.score == "softmax" else MOE_SCORE_SIGMOID
         if self.fp8:
             self.W = {k: self._quantise(weights[k]) for k in
                       ("W_gate_up", "W_down", "Ws_gate_up", "Ws_down")}
@@ -64,7 +79,8 @@ class MoELayer:
         self.topk_idx = torch.empty(T, K, dtype=torch.int32, device=dev)
         self.topk_gate = torch.empty(T, K, dtype=torch.float32, device=dev)
         self.counts = torch.zeros(N_r, dtype=torch.int32, device=dev)
-        self.route_ws = _ws(moe_route_workspace_size(T, N_r), dev)
+        self.route_ws = _ws(moe_route_scored_workspace_size(T, d, N_r) if c.scored
+                            else moe_route_workspace_size(T, N_r), dev)
         self.perm_ws = _ws(moe_permute_workspace_size(T, N_r), dev)
         self.x_perm = torch.empty(R, d, dtype=xdt, device=dev)
         self.offsets = torch.zeros(N_r + 1, dtype=torch.int32, device=dev)
@@ -92,6 +108,18 @@ class MoELayer:
             self.x_scale = torch.empty(R, d // 128, dtype=torch.float32, device=dev)
         self.T_alloc = T
 
+    def _route(self, u, stream, logits=None):
+        c = self.cfg
+        out = (self.topk_idx, self.topk_gate, self.counts, self.route_ws)
+        if c.scored:
+            moe_route_scored(u, self.E, self.b, c.K, *out, score=self.score, n_groups=c.n_groups,
+                             topk_groups=c.topk_groups, group_top=c.group_top, renorm=c.renorm,
+                             gate_scale=c.gate_scale, logits=logits, stream=stream)
+        elif c.n_groups > 1:
+            moe_route_grouped(u, self.E, self.b, c.K, c.n_groups, c.topk_groups, *out, stream)
+        else:
+            moe_route(u, self.E, self.b, c.K, *out, stream)
+
     # -- one step ------------------------------------------------------------
     def forward(self, u: torch.Tensor, stream=None, gate_up_events=None,
                 out: torch.Tensor | None = None, phase_events=None) -> torch.Tensor:
@@ -114,12 +142,7 @@ class MoELayer:
             if name in pe:
                 pe[name][i].record(st)
         mark("route", 0)
-        if c.n_groups > 1:
-            moe_route_grouped(u, self.E, self.b, c.K, c.n_groups, c.topk_groups, self.topk_idx,
-                              self.topk_gate, self.counts, self.route_ws, stream)
-        else:
-            moe_route(u, self.E, self.b, c.K, self.topk_idx, self.topk_gate, self.counts,
-                      self.route_ws, stream)
+        self._route(u, stream)
         mark("route", 1)
         mark("permute", 0)
         if self.fp8:
@@ -175,12 +198,18 @@ class MoELayer:
     def _alloc_train(self, T):
         c, dev = self.cfg, self.device
         R, bf = T * c.K, torch.bfloat16
-        self.a_gu = torch.empty(R, 2 * c.I, dtype=bf, device=dev)
         hdt = torch.uint8 if self.fp8 else bf
+        if c.checkpoint8:
+            # pre-activations as E4M3 codes and a scale for each row and 128 columns
+            pair = lambda rows: (torch.empty(rows, 2 * c.I, dtype=torch.uint8, device=dev),
+                                 torch.empty(rows, 2 * c.I // 128, dtype=torch.float32, device=dev))
+            self.a_gu, self.a_s = pair(R), [pair(T) for _ in range(c.N_s)]
+        else:
+            self.a_gu = torch.empty(R, 2 * c.I, dtype=bf, device=dev)
+            self.a_s = torch.empty(c.N_s, T, 2 * c.I, dtype=bf, device=dev)
         self.h_s = torch.empty(c.N_s, T, c.I, dtype=hdt, device=dev)
         self.h_s_scale = torch.empty(c.N_s, T, c.I // 128, dtype=torch.float32, device=dev) \
             if self.fp8 else None
-        self.a_s = torch.empty(c.N_s, T, 2 * c.I, dtype=bf, device=dev)
         self.dy_perm = torch.empty(R, c.d, dtype=bf, device=dev)
         self.d_gate = torch.empty(T, c.K, dtype=torch.float32, device=dev)
         self.d_logit = torch.empty(T, c.K, dtype=torch.float32, device=dev)
@@ -189,17 +218,36 @@ class MoELayer:
         self.dx_s = torch.empty(c.N_s, T, c.d, dtype=bf, device=dev)
         self.du = torch.empty(T, c.d, dtype=bf, device=dev)
         dt = MOE_E4M3 if self.fp8 else MOE_BF16
-        self.bwd_ws = _ws(max(moe_expert_ffn_backward_workspace_size(dt, R, c.d, c.I, c.N_r),
-                              moe_expert_ffn_backward_workspace_size(dt, T, c.d, c.I, 1)), dev)
+        size = moe_expert_ffn_backward8_workspace_size if c.checkpoint8 \
+            else moe_expert_ffn_backward_workspace_size
+        self.bwd_ws = _ws(max(size(dt, R, c.d, c.I, c.N_r), size(dt, T, c.d, c.I, 1)), dev)
+        if c.scored:
+            rdt = MOE_F32 if self.E.dtype == torch.float32 else MOE_BF16
+            self.logits = torch.empty(T, c.N_r, dtype=torch.float32, device=dev)
+            self.ones = torch.ones(T, c.K, dtype=torch.float32, device=dev)
+            self.route_bwd_ws = _ws(moe_route_scored_backward_workspace_size(rdt, T, c.d, c.N_r),
+                                    dev)
         if not hasattr(self, "grad"):
             self.grad = {k: torch.empty(self.W[k][0].shape, dtype=bf, device=dev) for k in
                          ("W_gate_up", "W_down", "Ws_gate_up", "Ws_down")}
             self.grad["E"] = torch.empty(c.N_r, c.d, dtype=torch.float32, device=dev)
         self.T_train = T
 
-    def forward_train(self, u: torch.Tensor, stream=None) -> torch.Tensor:
+    def _gate_up_save(self, x, offsets, wgu, h, keep, stream, x_scale=None, w_scale=None,
+                      h_scale=None):
+        if self.cfg.checkpoint8:
+            moe_expert_gate_up_save8(x, offsets, wgu, h, *keep, stream=stream)
+        else:
+            moe_expert_gate_up_save(x, offsets, wgu, h, keep, x_scale=x_scale,
+                                    w_scale_gate_up=w_scale, h_scale=h_scale, stream=stream)
+
+    def forward_train(self, u: torch.Tensor, stream=None,
+                      seq_offsets: torch.Tensor | None = None) -> torch.Tensor:
         """forward() that also keeps the gate/up pre-activations and h of the
-        routed and shared experts for backward().  bf16 and FP8 layers."""
+        routed and shared experts for backward().  bf16 and FP8 layers.  With
+        balance_alpha > 0, self.balance holds the balance loss of every
+        sequence [seq_offsets[q], seq_offsets[q+1]) of the tokens (int32 on the
+        device; default: one sequence of all of them)."""
         c = self.cfg
         if c.dtype not in ("bf16", "e4m3"):
             raise ValueError("the backward is implemented for bf16 and FP8 layers")
@@ -208,12 +256,7 @@ class MoELayer:
             self._alloc(T)
         if getattr(self, "T_train", None) != T:
             self._alloc_train(T)
-        if c.n_groups > 1:
-            moe_route_grouped(u, self.E, self.b, c.K, c.n_groups, c.topk_groups, self.topk_idx,
-                              self.topk_gate, self.counts, self.route_ws, stream)
-        else:
-            moe_route(u, self.E, self.b, c.K, self.topk_idx, self.topk_gate, self.counts,
-                      self.route_ws, stream)
+        self._route(u, stream, getattr(self, "logits", None))
         (wgu, sgu), (wdn, sdn) = self.W["W_gate_up"], self.W["W_down"]
         (wsgu, ssgu), (wsdn, ssdn) = self.W["Ws_gate_up"], self.W["Ws_down"]
         sl = lambda t, j: None if t is None else t[j:j + 1]
@@ -227,27 +270,53 @@ class MoELayer:
             moe_permute(u, self.topk_idx, c.N_r, self.x_perm, self.offsets, self.perm_src,
                         self.inv_row, self.perm_ws, stream=stream)
             x_sh, xs_sh = u, None
-        moe_expert_gate_up_save(self.x_perm, self.offsets, wgu, self.h_mid, self.a_gu,
-                                x_scale=self.x_scale if self.fp8 else None, w_scale_gate_up=sgu,
-                                h_scale=self.h_scale, stream=stream)
+        self._gate_up_save(self.x_perm, self.offsets, wgu, self.h_mid, self.a_gu, stream,
+                           self.x_scale if self.fp8 else None, sgu, self.h_scale)
         moe_expert_down(self.h_mid, self.offsets, wdn, self.y_perm, h_scale=self.h_scale,
                         w_scale_down=sdn, stream=stream)
         for j in range(c.N_s):
             hs_scale = None if self.h_s_scale is None else self.h_s_scale[j]
-            moe_expert_gate_up_save(x_sh, self.shared_offsets, wsgu[j:j + 1], self.h_s[j],
-                                    self.a_s[j], x_scale=xs_sh, w_scale_gate_up=sl(ssgu, j),
-                                    h_scale=hs_scale, stream=stream)
+            self._gate_up_save(x_sh, self.shared_offsets, wsgu[j:j + 1], self.h_s[j], self.a_s[j],
+                               stream, xs_sh, sl(ssgu, j), hs_scale)
             moe_expert_down(self.h_s[j], self.shared_offsets, wsdn[j:j + 1], self.y_shared[j],
                             h_scale=hs_scale, w_scale_down=sl(ssdn, j), stream=stream)
         moe_combine(u, self.y_shared if c.N_s else None, self.y_perm, self.inv_row,
                     self.topk_gate, self.h_out, stream)
+        if c.balance_alpha > 0:
+            self._balance(seq_offsets, stream)
         self._u = u
         return self.h_out
 
-    def backward(self, dh: torch.Tensor, stream=None, ffn_events=None) -> torch.Tensor:
+    def _balance(self, seq_offsets, stream):
+        c, T = self.cfg, self.T_train
+        n = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+        if getattr(self, "_balance_for", None) != (T, n):
+            self.balance = torch.empty(n, dtype=torch.float32, device=self.device)
+            self.balance_coef = torch.empty(n, c.N_r, dtype=torch.float32, device=self.device)
+            self.balance_ws = _ws(moe_balance_loss_workspace_size(T, c.N_r, n), self.device)
+            self._balance_for = (T, n)
+        moe_balance_loss(self.logits, self.topk_idx, c.balance_alpha, self.balance,
+                         self.balance_coef, self.balance_ws, score=self.score,
+                         seq_offsets=seq_offsets, stream=stream)
+        self.seq_offsets = seq_offsets
+
+    def _ffn_backward(self, x, offsets, wgu, wdn, keep, h, dy, dx, dwgu, dwdn, stream, x_rows=None,
+                      sgu=None, sdn=None):
+        if self.cfg.checkpoint8:
+            moe_expert_ffn_backward8(x, offsets, wgu, wdn, *keep, dy, dx, dwgu, dwdn, self.bwd_ws,
+                                     stream=stream)
+        else:
+            moe_expert_ffn_backward(x, offsets, wgu, wdn, keep, h, dy, dx, dwgu, dwdn, self.bwd_ws,
+                                    x_rows=x_rows, w_scale_gate_up=sgu, w_scale_down=sdn,
+                                    stream=stream)
+
+    def backward(self, dh: torch.Tensor, stream=None, ffn_events=None,
+                 d_balance: torch.Tensor | None = None) -> torch.Tensor:
         """Gradients for upstream dh = dL/dh' of the last forward_train:
         returns du (overwritten by the next call) and fills self.grad
         (E: float32; W_gate_up, W_down, Ws_gate_up, Ws_down: bf16).
+        d_balance [n_seq] float32: dL/dself.balance (default 1 for every
+        sequence) where the configuration has a balance loss.
         ffn_events=(start, end) records CUDA events around the routed expert
         FFN backward on the same stream."""
         c, g = self.cfg, self.grad
@@ -266,19 +335,29 @@ class MoELayer:
             x_r, x_rows, h_r = u, self.perm_src, None
         else:
             x_r, x_rows, h_r = self.x_perm, None, self.h_mid
-        moe_expert_ffn_backward(x_r, self.offsets, wgu, wdn, self.a_gu, h_r, self.dy_perm,
-                                self.dx_perm, g["W_gate_up"], g["W_down"], self.bwd_ws,
-                                x_rows=x_rows, w_scale_gate_up=sgu, w_scale_down=sdn,
-                                stream=stream)
+        self._ffn_backward(x_r, self.offsets, wgu, wdn, self.a_gu, h_r, self.dy_perm,
+                           self.dx_perm, g["W_gate_up"], g["W_down"], stream, x_rows, sgu, sdn)
         if ffn_events:
             ffn_events[1].record(st)
         for j in range(c.N_s):
-            moe_expert_ffn_backward(u, self.shared_offsets, wsgu[j:j + 1], wsdn[j:j + 1],
-                                    self.a_s[j], None if self.fp8 else self.h_s[j], dh,
-                                    self.dx_s[j], g["Ws_gate_up"][j:j + 1],
-                                    g["Ws_down"][j:j + 1], self.bwd_ws,
-                                    w_scale_gate_up=sl(ssgu, j), w_scale_down=sl(ssdn, j),
-                                    stream=stream)
+            self._ffn_backward(u, self.shared_offsets, wsgu[j:j + 1], wsdn[j:j + 1], self.a_s[j],
+                               None if self.fp8 else self.h_s[j], dh, self.dx_s[j],
+                               g["Ws_gate_up"][j:j + 1], g["Ws_down"][j:j + 1], stream, None,
+                               sl(ssgu, j), sl(ssdn, j))
+        if c.scored:
+            # residual, shared and routed gradients (the combine with weights
+            # 1), then the router's own added in place
+            moe_combine(dh, self.dx_s if c.N_s else None, self.dx_perm, self.inv_row, self.ones,
+                        self.du, stream)
+            bal = c.balance_alpha > 0
+            moe_route_scored_backward(u, self.E, self.logits, self.topk_idx, self.d_gate, self.du,
+                                      g["E"], self.route_bwd_ws, score=self.score,
+                                      renorm=c.renorm, gate_scale=c.gate_scale,
+                                      seq_offsets=self.seq_offsets if bal else None,
+                                      balance_coef=self.balance_coef if bal else None,
+                                      d_loss=d_balance if bal else None, du_base=self.du,
+                                      stream=stream)
+            return self.du
         moe_unpermute_backward(dh, self.dx_s if c.N_s else None, self.dx_perm, self.inv_row,
                                self.topk_idx, self.d_logit, self.E, self.du, stream)
         if self.fp8:

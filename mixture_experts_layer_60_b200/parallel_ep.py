@@ -26,7 +26,8 @@ import torch
 
 from . import (moe_combine, moe_ep_dispatch, moe_ep_plan, moe_ep_return, moe_expert_ffn,
                moe_expert_ffn_workspace_size, moe_permute_index, moe_permute_workspace_size,
-               moe_route, moe_route_workspace_size, MOE_BF16, MOE_F32)
+               moe_route, moe_route_scored, moe_route_scored_workspace_size,
+               moe_route_workspace_size, MOE_BF16, MOE_F32, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX)
 from .configs import LayerConfig
 
 
@@ -68,7 +69,8 @@ class _EPRank:
         self.topk_idx = torch.empty(T_max, c.K, dtype=torch.int32, device=dev)
         self.topk_gate = torch.empty(T_max, c.K, dtype=torch.float32, device=dev)
         self.counts = torch.zeros(c.N_r, dtype=torch.int32, device=dev)
-        self.route_ws = _ws(moe_route_workspace_size(T_max, c.N_r), dev)
+        self.route_ws = _ws(moe_route_scored_workspace_size(T_max, c.d, c.N_r) if c.scored
+                            else moe_route_workspace_size(T_max, c.N_r), dev)
         self.perm_ws = _ws(moe_permute_workspace_size(T_max, c.N_r), dev)
         self.offsets = torch.zeros(c.N_r + 1, dtype=torch.int32, device=dev)
         self.perm_src = torch.empty(R, dtype=torch.int32, device=dev)
@@ -96,8 +98,15 @@ class _EPRank:
         self.shared_offsets.fill_(T)
         self.shared_offsets[0] = 0
         self.u = u
-        moe_route(u, self.E, self.b, c.K, self.topk_idx[:T], self.topk_gate[:T], self.counts,
-                  self.route_ws, stream)
+        out = (self.topk_idx[:T], self.topk_gate[:T], self.counts, self.route_ws)
+        if c.scored:
+            moe_route_scored(u, self.E, self.b, c.K, *out,
+                             score=MOE_SCORE_SOFTMAX if c.score == "softmax" else MOE_SCORE_SIGMOID,
+                             n_groups=c.n_groups, topk_groups=c.topk_groups,
+                             group_top=c.group_top, renorm=c.renorm, gate_scale=c.gate_scale,
+                             stream=stream)
+        else:
+            moe_route(u, self.E, self.b, c.K, *out, stream)
         # the grouping only: moe_ep_dispatch copies the rows from u itself
         moe_permute_index(self.topk_idx[:T], c.N_r, self.offsets, self.perm_src[:T * c.K],
                           self.inv_row[:T], self.perm_ws, stream=stream)

@@ -167,3 +167,13 @@ def test_oracle_checkpoint_rounds_to_nearest():
     t = torch.from_numpy(np.linspace(-460, 460, 40001).astype(np.float32))
     assert np.array_equal(S.e4m3(t.numpy()),
                           t.clamp(-448, 448).to(torch.float8_e4m3fn).double().numpy())
+
+
+def test_a_workspace_for_more_tokens_serves_fewer(L):
+    for N in (16, 61, 256, 257, 1024):
+        for size in (lambda T: L.moe_route_scored_workspace_size(T, 7168, N),
+                     lambda T: L.moe_balance_loss_workspace_size(T, N, 9),
+                     lambda T: L.moe_route_scored_backward_workspace_size(1, T, 7168, N),
+                     lambda T: L.moe_route_scored_backward_workspace_size(0, T, 7168, N)):
+            at = [size(T) for T in list(range(1, 700, 13)) + list(range(700, 20500, 97))]
+            assert all(a <= b for a, b in zip(at, at[1:]))
