@@ -937,12 +937,10 @@ moe_status moe_expert_gate_up_save8(const void* x, const int32_t* offsets, int n
 
 namespace {
 
-// Backward workspace from an 8-bit checkpoint: dA [rows, 2I] bf16, h [rows, I]
-// bf16, then the weight gradients' tail blocks.
+// Backward workspace from an 8-bit checkpoint: dA [rows, 2I] and h [rows, I] bf16.
 size_t ffn_bwd8_ws(moe_dtype dt, int rows, int d, int I, int G) {
   if (dt != MOE_BF16 || rows <= 0 || d <= 0 || I <= 0 || G <= 0) return 0;
-  return align_up((size_t)rows * 2 * I * 2, 256) + align_up((size_t)rows * I * 2, 256) +
-         wgrad_tail_bytes((size_t)(d > 2 * I ? d : 2 * I) * 2, 64, G);
+  return align_up((size_t)rows * 2 * I * 2, 256) + align_up((size_t)rows * I * 2, 256);
 }
 
 }  // namespace
@@ -982,13 +980,12 @@ moe_status moe_expert_ffn_backward8(const void* x, const int32_t* offsets, int n
   uint8_t* w = static_cast<uint8_t*>(workspace);
   void* dA = w;
   void* h = w + align_up((size_t)rows * 2 * I * 2, 256);
-  void* tail = static_cast<uint8_t*>(h) + align_up((size_t)rows * I * 2, 256);
   // Dgrad of the down projection fused with the SwiGLU backward -> dA, h
   MOE_TRY(launch_ws_dswiglu8(dy, W_down, offsets, n_groups, rows, I, d, a_q, a_scale, dA, h, s));
-  MOE_TRY(launch_wgrad_gemm(dy, d, h, I, offsets, n_groups, rows, tail, dW_down, s, true));
+  MOE_TRY(launch_wgrad_pair(dy, d, h, I, offsets, n_groups, rows, dW_down, s));
   MOE_TRY(launch_ws_gemm_ex(dA, W_gate_up, 0, offsets, n_groups, rows, d, 2 * I, WS_STORE, true,
                             dx, d, nullptr, 0, s, nullptr, true));
-  return launch_wgrad_gemm(dA, 2 * I, x, d, offsets, n_groups, rows, tail, dW_gate_up, s, true);
+  return launch_wgrad_pair(dA, 2 * I, x, d, offsets, n_groups, rows, dW_gate_up, s);
 }
 
 // ---------------------------------------------------------------- expert parallelism

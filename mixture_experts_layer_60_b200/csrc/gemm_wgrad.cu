@@ -111,8 +111,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_wait();                  // launched with `after`: the setup overlaps the kernel before
-  pdl_trigger();
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp == 0) {
@@ -287,8 +285,6 @@ __global__ void __launch_bounds__(256) wgrad_tails_kernel(const uint4* __restric
                                                           const int32_t* __restrict__ offsets,
                                                           int rows, uint4* __restrict__ T) {
   const int g = blockIdx.x, i = blockIdx.y;
-  pdl_wait();
-  pdl_trigger();
   int r0, r1;
   clamp_group_rows(offsets, g, rows, nullptr, r0, r1);   // the GEMM reports a clamp
   const int cnt = r1 - r0;
@@ -307,14 +303,10 @@ __global__ void __launch_bounds__(256) wgrad_tails_kernel(const uint4* __restric
 
 moe_status launch_wgrad_tails(const void* A, size_t row_bytes, int block_rows,
                               const int32_t* offsets, int n_groups, int rows, void* T,
-                              cudaStream_t s, bool after) {
+                              cudaStream_t s) {
   const int G = offsets ? n_groups : 1;
   if (G <= 0 || rows <= 0) return MOE_OK;
   dim3 grid(G, block_rows);
-  if (after)
-    return launch_after(wgrad_tails_kernel, grid, dim3(256), 0, s, 1, "wgrad tails launch",
-                        static_cast<const uint4*>(A), (int)(row_bytes / 16), block_rows, offsets,
-                        rows, static_cast<uint4*>(T));
   wgrad_tails_kernel<<<grid, 256, 0, s>>>(static_cast<const uint4*>(A), (int)(row_bytes / 16),
                                           block_rows, offsets, rows, static_cast<uint4*>(T));
   return cuda_check(cudaGetLastError(), "wgrad tails launch");
@@ -325,8 +317,7 @@ size_t wgrad_tail_bytes(size_t row_bytes, int block_rows, int n_groups) {
 }
 
 moe_status launch_wgrad_gemm(const void* A, int M, const void* B, int N, const int32_t* offsets,
-                             int n_groups, int rows, void* A_tail, void* C, cudaStream_t s,
-                             bool after) {
+                             int n_groups, int rows, void* A_tail, void* C, cudaStream_t s) {
   const int G = offsets ? n_groups : 1;
   if (G <= 0) return MOE_OK;
   if (M % BM || N % BN)
@@ -337,7 +328,7 @@ moe_status launch_wgrad_gemm(const void* A, int M, const void* B, int N, const i
     return cuda_check(cudaMemsetAsync(C, 0, (size_t)G * M * N * 2, s), "wgrad zero fill");
   }
   // the A operand's tail blocks: [G * BK rows][M] (launch_wgrad_tails)
-  moe_status st = launch_wgrad_tails(A, (size_t)M * 2, BK, offsets, G, rows, A_tail, s, after);
+  moe_status st = launch_wgrad_tails(A, (size_t)M * 2, BK, offsets, G, rows, A_tail, s);
   if (st != MOE_OK) return st;
   CUtensorMap tmA, tmB, tmC, tmAt;
   st = make_tmap_col_blocks(&tmA, A, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, M, rows, 64, BK, BM / 64);
@@ -369,9 +360,6 @@ moe_status launch_wgrad_gemm(const void* A, int M, const void* B, int N, const i
   const long long tiles = (long long)G * (M / BM) * (N / BN);
   int grid = sm_count();
   if (tiles < grid) grid = (int)tiles;
-  if (after)
-    return launch_after(wgrad_gemm_kernel, dim3(grid), dim3(kThreads), SMEM_ALLOC, s, 1,
-                        "wgrad gemm launch", tmA, tmB, tmC, tmAt, p);
   wgrad_gemm_kernel<<<grid, kThreads, SMEM_ALLOC, s>>>(tmA, tmB, tmC, tmAt, p);
   return cuda_check(cudaGetLastError(), "wgrad gemm launch");
 }

@@ -334,6 +334,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
+moe_status launch_wgrad_tails(const void* A, size_t row_bytes, int block_rows,
+                              const int32_t* offsets, int n_groups, int rows, void* T,
+                              cudaStream_t s);
 
 moe_status launch_wgrad_fp8(const void* qa, const float* sa, int M, const void* qb,
                             const float* sb, int N, const int32_t* offsets, int n_groups,

@@ -123,8 +123,8 @@ moe_status launch_ws2_gemm(const void* X, const void* W, int b_rows_per_group,
 //            DSWIGLU dh = the product (N = I columns), a = S[:, 0:I], b = S[:, I:2I]:
 //                    C[:, 0:I] = dh * b * SiLU'(a), C[:, I:2I] = dh * SiLU(a).
 // w_mn: W is stored [G*K rows][N cols] (N contiguous) instead of [G*rows_per_group][K].
-// after (WS_STORE with w_mn; the weight gradients below too): launched over the
-// tail of the stream's previous kernel (launch_after).
+// after (WS_STORE with w_mn): launched over the tail of the stream's previous
+// kernel (launch_after).
 enum WsEpi { WS_SWIGLU = 0, WS_STORE = 1, WS_SWIGLU_SAVE = 2, WS_DSWIGLU = 3,
              WS_SWIGLU_SAVE8 = 4, WS_DSWIGLU8 = 5 };   // the 8s: by their own launchers below
 moe_status launch_ws_gemm_ex(const void* X, const void* W, int b_rows_per_group,
@@ -166,13 +166,18 @@ moe_status launch_gather_pipe(int mode, moe_dtype dt, const void* a, const void*
 // A_tail: scratch of wgrad_tail_bytes(M * 2, 64, groups) bytes for the groups'
 // zero-padded last 64-row blocks of A.
 moe_status launch_wgrad_gemm(const void* A, int M, const void* B, int N, const int32_t* offsets,
-                             int n_groups, int rows, void* A_tail, void* C, cudaStream_t s,
-                             bool after = false);
+                             int n_groups, int rows, void* A_tail, void* C, cudaStream_t s);
 // T[g] = the last block_rows-row block of group g of A (rows past the group zeroed).
 moe_status launch_wgrad_tails(const void* A, size_t row_bytes, int block_rows,
                               const int32_t* offsets, int n_groups, int rows, void* T,
-                              cudaStream_t s, bool after = false);
+                              cudaStream_t s);
 size_t wgrad_tail_bytes(size_t row_bytes, int block_rows, int n_groups);
+
+// gemm_wgrad_pair.cu --------------------------------------------------------------
+// The same product on CTA pairs (M and N multiples of 256); rows past a group's
+// end may hold anything.  Launched over the tail of the stream's previous kernel.
+moe_status launch_wgrad_pair(const void* A, int M, const void* B, int N, const int32_t* offsets,
+                         int n_groups, int rows, void* C, cudaStream_t s);
 
 // gemm_wgrad_fp8.cu ----------------------------------------------------------
 // C[g] [M, N] = sum over g's 128-row blocks b of (qa_b^T qb_b) * sa[b, m] * sb[b, n].

@@ -172,6 +172,49 @@ def test_backward8_is_the_plain_backward_for_exact_checkpoints():
     assert torch.equal(dx, ref[0]) and torch.equal(dWgu, ref[1])
 
 
+def test_backward8_keeps_groups_apart():
+    """Rows of another group, and rows behind the last one, may hold anything: NaN there stays out
+    of a group's gradients.  Rows outside every group are not written."""
+    sizes, d, I = [37, 5, 0, 130, 1, 64], 256, 512
+    x, off, Wgu, Wdn, dy = _ffn(sizes + [50], d, I, 12)
+    off = off[:-1].contiguous()                   # the last 50 rows belong to no group
+    Wgu, Wdn = Wgu[:-1].contiguous(), Wdn[:-1].contiguous()
+    h, q, sc = _save8(x, off, Wgu, 0)
+    (dx, dWgu, dWdn), _ = _backward8(x, off, Wgu, Wdn, q, sc, dy)
+    n = int(off[-1])
+    assert torch.isfinite(dWgu).all() and torch.isfinite(dWdn).all()
+    assert torch.isnan(dx[n:]).all() and torch.isfinite(dx[:n]).all()
+    bx, bdy, bsc = x.clone(), dy.clone(), sc.clone()
+    for t in (bx, bdy, bsc):
+        t[n:] = float("nan")                      # behind the last group
+        t[37:42] = float("nan")                   # all of group 1
+    (ex, egu, edn), _ = _backward8(bx, off, Wgu, Wdn, q, bsc, bdy)
+    keep = [e for e in range(len(sizes)) if e != 1]
+    assert torch.equal(egu[keep], dWgu[keep]) and torch.equal(edn[keep], dWdn[keep])
+    assert torch.isnan(egu[1]).all() and torch.isnan(edn[1]).all()
+    rows = [r for r in range(n) if not 37 <= r < 42]
+    assert torch.equal(ex[rows], dx[rows])
+
+
+def test_backward8_many_small_groups():
+    """Groups of fewer rows than a stage, one after the other in the ring."""
+    rng = np.random.default_rng(2)
+    sizes = rng.integers(0, 20, 150).tolist()
+    x, off, Wgu, Wdn, dy = _ffn(sizes, 256, 256, 13)
+    h, q, sc = _save8(x, off, Wgu)
+    (dx, dWgu, dWdn), _ = _backward8(x, off, Wgu, Wdn, q, sc, dy)
+    a = S.from_checkpoint(f64(_values(q)), f64(sc))
+    o = off.tolist()
+    for e in range(len(sizes)):
+        r = slice(o[e], o[e + 1])
+        if sizes[e] == 0:
+            assert not dWgu[e].any() and not dWdn[e].any()
+            continue
+        want = S.ffn_backward(f64(x[r]), f64(Wgu[e]), f64(Wdn[e]), a[r], f64(dy[r]))
+        for got, ref in ((dx[r], want[0]), (dWgu[e], want[1]), (dWdn[e], want[2])):
+            assert np.linalg.norm(f64(got) - ref) <= 2.0 ** -7 * np.linalg.norm(ref)
+
+
 def test_checkpoint8_streams_and_graphs():
     sizes, d, I = [70, 5, 130], 256, 256
     x, off, Wgu, Wdn, dy = _ffn(sizes, d, I, 11)
