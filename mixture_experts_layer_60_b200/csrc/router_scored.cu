@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(MAXT) router_token_kernel(
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ double part[MAXT / 32][kDots];
   __shared__ int n_want;
-  __shared__ double red[33];
+  __shared__ uint32_t red[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = r.N_r, nv = d / 8;
   const BlockRoute b = block_route_smem(smem_raw, N, r.K);
   pdl_wait();
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(MAXT) router_token_kernel(
     }
     float logit_err = 0.f;
     if (!EXACT) {
-      mag = (float)block_reduce((double)mag, false, red);
+      mag = __uint_as_float(block_max(__float_as_uint(mag), red));
       logit_err = mag == 0.f ? 0.f : kLogitError * fmaxf(4.f, mag);
     }
     if (tid < N) {

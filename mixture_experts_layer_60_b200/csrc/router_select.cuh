@@ -363,15 +363,21 @@ __device__ __forceinline__ BlockRoute block_route_smem(uint8_t* p, int N, int K)
   return b;
 }
 
-// Sum or largest of v over the block, in warp order (red: 33 doubles).
-__device__ __forceinline__ double block_reduce(double v, bool sum, double* red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  v = sum ? sel_warp_sum(v) : sel_warp_max(v);
+// Sum of v over the block, in warp order; largest of a whole number.  red: 32
+// of its kind, not touched again before the block's next barrier but one.
+__device__ __forceinline__ double block_sum(double v, double* red) {
+  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  v = sel_warp_sum(v);
+  if (lane == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  if (lane == 0) red[warp] = v;
+  return sel_warp_sum(lane < nw ? red[lane] : 0.0);
+}
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
+  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  v = __reduce_max_sync(0xffffffffu, v);
+  if (lane == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = lane < nw ? red[lane] : (sum ? 0.0 : -(double)INFINITY);
-  return sum ? sel_warp_sum(v) : sel_warp_max(v);
+  return __reduce_max_sync(0xffffffffu, lane < nw ? red[lane] : 0u);
 }
 
 // Routes one token by the whole block; false: exact scores that only the error
@@ -387,7 +393,8 @@ __device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRul
                                             Fetch fetch, int32_t* __restrict__ idx,
                                             float* __restrict__ gate,
                                             int32_t* __restrict__ counts) {
-  __shared__ double red[33];
+  __shared__ double red_z[32];
+  __shared__ uint32_t red_m[32], red_w[32], red_s[32];
   __shared__ float gkey[32][2];
   __shared__ unsigned s_near;
   __shared__ int n_list, s_lo, s_hi;
@@ -402,18 +409,25 @@ __device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRul
     const bool ex = mine && b.exact_f[e];
     const bool all = __syncthreads_and(!mine || ex);
     const double x = mine ? b.x[e] : 0.0;
+    // scores: float64 for exact logits, float32 (expf and division: within
+    // 4 * 2^-23 of themselves) for the others
+    float s = 0.f;
     if (softmax) {
-      m = block_reduce(mine ? x : -(double)INFINITY, false, red);
-      z = block_reduce(mine ? exp(x - m) : 0.0, true, red);
+      m = (double)sel_val(block_max(mine ? sel_ord((float)x) : 0u, red_m));
+      const double ev = !mine ? 0.0 : ex ? exp(x - m) : (double)expf((float)(x - m));
+      z = block_sum(ev, red_z);
+      if (mine) s = ex ? (float)(ev / z) : (float)ev / (float)z;
+    } else if (mine) {
+      s = ex ? (float)sel_sigmoid(x) : sel_sigmoid((float)x);
     }
-    const float s = mine ? (float)(softmax ? exp(x - m) / z : sel_sigmoid(x)) : 0.f;
     const float key = bias ? s + bi : s;
     // error of the inexact keys, and of the softmax's sum, which exact keys share
     float err = 0.f, eta = 0.f, smax = 0.f;
     if (!all) {
-      const float w = (float)block_reduce((double)(s * (1.f - s)), false, red);
-      smax = (float)block_reduce((double)s, false, red);
-      err = logit_err * w * (softmax ? 2.f : 1.f) + 1.2e-7f * smax;
+      // non-negative floats compare as whole numbers (fmaxf drops a NaN)
+      const float w = __uint_as_float(block_max(__float_as_uint(fmaxf(0.f, s * (1.f - s))), red_w));
+      smax = __uint_as_float(block_max(__float_as_uint(fmaxf(0.f, s)), red_s));
+      err = logit_err * w * (softmax ? 2.f : 1.f) + 4.8e-7f * smax;
       eta = softmax ? logit_err : 0.f;
     }
     const float rel = err > 0.f ? kKeyRounding : 0.f;
