@@ -73,6 +73,14 @@ struct DeParams {
   int* err;
 };
 
+// Column col (a multiple of 4) of a segment's row: [row / 32][col / 8][32][8], so
+// that the 32 bytes which a lane (one row) writes at a time lie side by side
+// over the warp.
+__device__ __forceinline__ size_t seg_at(int seg, int row, int col) {
+  return (size_t)seg * 256 * BN + (row >> 5) * (32 * BN) + (col >> 3) * 256 + (row & 31) * 8 +
+         (col & 7);
+}
+
 // First unit of pair c of P over U units.
 __host__ __device__ __forceinline__ int first_unit(int c, int P, int U) {
   return (int)((long long)c * U / P);
@@ -236,11 +244,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // experts past N_r are zero rows: not kept
       const int row = (int)half * 128 + q * 32 + lane;
       if (tile / p.n_slab * 256 + row < p.N_r) {
-        float* out = p.C + ((size_t)(pair + tile) * 256 + row) * BN + part * 64;
+        float* out = p.C + seg_at(pair + tile, row, part * 64);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          st_global_v8(out + i * 16, &acc[i][0]);
-          st_global_v8(out + i * 16 + 8, &acc[i][8]);
+          st_global_v8(out + i * 512, &acc[i][0]);
+          st_global_v8(out + i * 512 + 256, &acc[i][8]);
         }
       }
       un = k1;
@@ -255,8 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Adds a tile's segments in order: a block per tile and kJoinRows of its rows,
-// a float4 of 64 columns-of-four per thread.
+// Adds a tile's segments in order: a block per tile and kJoinRows of its rows;
+// a warp takes all of the rows by 16 columns, so that it reads runs of 256 bytes.
 constexpr int kJoinRows = 8;
 __global__ void __launch_bounds__(256) router_de_join_kernel(const float* __restrict__ C, int P,
                                                              int nk, int n_slab, int units,
@@ -276,12 +284,14 @@ __global__ void __launch_bounds__(256) router_de_join_kernel(const float* __rest
     s_c1 = c1;
   }
   __syncthreads();
-  const int c0 = s_c0, c1 = s_c1, c4 = (threadIdx.x & 63) * 4;
+  const int c0 = s_c0, c1 = s_c1, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kJoinRows + ((lane >> 1) & 7);
+  if (e0 + row >= N_r) return;
 #pragma unroll
-  for (int k = 0; k < kJoinRows / 4; ++k) {
-    const int row = blockIdx.y * kJoinRows + k * 4 + (threadIdx.x >> 6);
-    if (e0 + row >= N_r || slab * BN + c4 >= d) continue;
-    const float* src = C + ((size_t)(c0 + tile) * 256 + row) * BN + c4;
+  for (int k = 0; k < 2; ++k) {
+    const int col = (threadIdx.x >> 5) * 16 + k * 128 + (lane >> 4) * 8 + (lane & 1) * 4;
+    if (slab * BN + col >= d) continue;
+    const float* src = C + seg_at(c0 + tile, row, col);
     float4 a = *reinterpret_cast<const float4*>(src);
 #pragma unroll 4
     for (int c = c0 + 1; c < c1; ++c) {
@@ -289,7 +299,7 @@ __global__ void __launch_bounds__(256) router_de_join_kernel(const float* __rest
       const float4 b = *reinterpret_cast<const float4*>(src);
       a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
     }
-    *reinterpret_cast<float4*>(dE + (size_t)(e0 + row) * d + slab * BN + c4) = a;
+    *reinterpret_cast<float4*>(dE + (size_t)(e0 + row) * d + slab * BN + col) = a;
   }
 }
 

@@ -2,13 +2,14 @@
 // and group-limited top-K, gates, load.
 //
 // Logits come as S partial sums over slices of d, [S][T][ld]:
-//   float32 inputs: float64 on CUDA cores (router_logits64_kernel);
+//   float32 inputs: float64 on the tensor cores' float64 pipe (router_logits64_kernel);
 //   few bf16 tokens: float64, a block per expert (router_logits_few_kernel);
 //   else bf16 on tcgen05 CTA pairs, float32 (router_logits_tc_kernel).
-// A warp per token joins the slices and routes (router_select.cuh).  From
-// float64 logits the keys are the definition's; from float32 ones the tokens
-// with a close decision are listed and routed again from float64 logits of
-// the experts that can take part in it (router_recheck_kernel).
+// A block or a warp per token joins the slices and routes (router_select.cuh).
+// From float64 logits the keys are the definition's; from float32 ones a
+// decision too close for them is made again from float64 logits of the experts
+// that can take part in it: by the token's block, or, where warps route, by a
+// block for each token that they listed (router_token_kernel).
 //
 // Every wait is bounded (1 s of %globaltimer) and reported through the device
 // error word.
@@ -57,11 +58,24 @@ constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 16;
 constexpr int SMEM_ALLOC = SMEM_BYTES + 1024;
 
+// Partial logits of the tensor-core path: groups of 32 tokens, [ld / 8][32][8]
+// each, so that the 32 bytes which a lane (one token) writes at a time lie side
+// by side over the warp: in rows of ld every store touches 32 lines, 1.5 us
+// more whatever T.
+__host__ __device__ __forceinline__ int token_groups(int T) { return T / 32 + (T % 32 != 0); }
+__host__ __device__ __forceinline__ size_t slice_stride(int T, int ld) {
+  return (size_t)token_groups(T) * 32 * ld;
+}
+__device__ __forceinline__ size_t tc_row(int t, int ld) {
+  return (size_t)(t >> 5) * 32 * ld + (t & 31) * 8;
+}
+__device__ __forceinline__ int tc_col(int e) { return (e >> 3) * 256 + (e & 7); }
+
 struct LogitParams {
   int T, N_r, nk, S;
   int n_tt, n_et, Nt;       // token tiles of 256, expert tiles of Nt
   int ld;                   // n_et * Nt
-  float* P;                 // [S][T][ld]
+  float* P;                 // S slices of groups of 32 tokens (tc_row)
   int32_t* counts;          // zeroed here, as is the listing's length
   int32_t* n_listed;        // two lengths
   int* err;
@@ -243,13 +257,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!ok) break;
       const int t = tt * 2 * TM + (int)half * TM + q * 32 + lane;
       if (t < p.T) {
-        float* out = p.P + ((size_t)sl * p.T + t) * p.ld + et * Nt;
+        float* out = p.P + sl * slice_stride(p.T, p.ld) + tc_row(t, p.ld) + tc_col(et * Nt);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
           const int piece = part + i * (kEpiWarps / 4);
           if (piece < n_pieces) {
-            st_global_v8(out + piece * 16, &acc[i][0]);
-            st_global_v8(out + piece * 16 + 8, &acc[i][8]);
+            st_global_v8(out + piece * 512, &acc[i][0]);
+            st_global_v8(out + piece * 512 + 256, &acc[i][8]);
           }
         }
       }
@@ -480,14 +494,14 @@ __device__ __forceinline__ float join_slices(const float* __restrict__ row, int 
   float m[V], mag = 0.f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    x[j] = j * 32 + lane < N ? row[j * 32 + lane] : 0.f;
+    x[j] = j * 32 + lane < N ? row[tc_col(j * 32 + lane)] : 0.f;
     m[j] = fabsf(x[j]);
   }
   for (int s = 1; s < S; ++s) {
     row += stride;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const float v = j * 32 + lane < N ? row[j * 32 + lane] : 0.f;
+      const float v = j * 32 + lane < N ? row[tc_col(j * 32 + lane)] : 0.f;
       x[j] += v;
       m[j] += fabsf(v);
     }
@@ -512,7 +526,7 @@ __global__ void __launch_bounds__(128) router_select_kernel(
   pdl_trigger();
   for (int t = blockIdx.x * wpb + warp; t < T; t += gridDim.x * wpb) {
     float x[V], sc[V], key[V];
-    const float mag = sel_warp_max(join_slices<V>(P + (size_t)t * ld, S, (size_t)T * ld, N, x));
+    const float mag = sel_warp_max(join_slices<V>(P + tc_row(t, ld), S, slice_stride(T, ld), N, x));
     if (logits) {
 #pragma unroll
       for (int j = 0; j < V; ++j)
@@ -548,16 +562,22 @@ __global__ void __launch_bounds__(128) router_select_kernel(
 // the listed ones (rc.tok, the first pass left their decisions open).
 //   EXACT   P holds float64 slices
 //   else    float32 slices; the experts that open decisions wait for get
-//           float64 logits, eight at a time, their products spread over the
+//           float64 logits, kDots at a time, their products spread over the
 //           block (exact in float32 unless below 2^-126).  Usually two or
 //           three experts and one turn.
-constexpr int kDots = 8;
+// Latency-bound (at T 8192 some 50 tokens are listed), so a thread has two
+// vectors of every row in flight at once (one where a block has more threads
+// than 256); four of them, or more registers than let three blocks share an
+// SM, cost more tokens what they save few: T 1024 55 us, T 256 26 against 36
+// and 23.
+constexpr int kDots = 4;
 template <bool EXACT, int MAXT>
-__global__ void __launch_bounds__(MAXT) router_token_kernel(
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) router_token_kernel(
     const __nv_bfloat16* __restrict__ u, const __nv_bfloat16* __restrict__ E,
     const void* __restrict__ P, int S, int ld, const float* __restrict__ bias, int T, int d,
     SelectRule r, int32_t* __restrict__ idx, float* __restrict__ gate,
     int32_t* __restrict__ counts, float* __restrict__ logits, Recheck rc, bool all_tokens) {
+  constexpr int kAhead = MAXT <= 256 ? 2 : 1;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ double part[MAXT / 32][kDots];
   __shared__ int n_want;
@@ -572,11 +592,12 @@ __global__ void __launch_bounds__(MAXT) router_token_kernel(
     double a = 0.0;
     float mag = 0.f;
     if (tid < N) {
-      const size_t at = (size_t)t * ld + tid, stride = (size_t)T * ld;
       if (EXACT) {
+        const size_t at = (size_t)t * ld + tid, stride = (size_t)T * ld;
         for (int s = 0; s < S; ++s) a += static_cast<const double*>(P)[at + s * stride];
       } else {
         // as the first pass joined them
+        const size_t at = tc_row(t, ld) + tc_col(tid), stride = slice_stride(T, ld);
         float f = static_cast<const float*>(P)[at];
         mag = fabsf(f);
         for (int s = 1; s < S; ++s) {
@@ -598,28 +619,38 @@ __global__ void __launch_bounds__(MAXT) router_token_kernel(
       b.exact_f[tid] = EXACT || mag == 0.f;
     }
     const auto fetch = [&](int nl) {
+      if (EXACT) return;                            // nothing is wanted
       const uint4* ur = reinterpret_cast<const uint4*>(u + (size_t)t * d);
       for (int c0 = 0; c0 < nl; c0 += kDots) {
         const int nc = min(kDots, nl - c0);
+        const uint4* er[kDots];
         double acc[kDots];
 #pragma unroll
-        for (int c = 0; c < kDots; ++c) acc[c] = 0.0;
-        for (int v = tid; v < nv; v += blockDim.x) {
-          float fx[8];
-          Vec<__nv_bfloat16>::load(__ldg(ur + v), fx);
-          uint4 y[kDots];
+        for (int c = 0; c < kDots; ++c) {
+          er[c] = reinterpret_cast<const uint4*>(E + (size_t)b.list[c0 + min(c, nc - 1)] * d);
+          acc[c] = 0.0;
+        }
+        for (int v0 = tid; v0 < nv; v0 += kAhead * blockDim.x) {
+          uint4 x[kAhead], y[kAhead][kDots];
 #pragma unroll
-          for (int c = 0; c < kDots; ++c)
-            y[c] = c < nc
-                       ? __ldg(reinterpret_cast<const uint4*>(E + (size_t)b.list[c0 + c] * d) + v)
-                       : make_uint4(0, 0, 0, 0);
+          for (int a = 0; a < kAhead; ++a) {
+            const int v = v0 + a * blockDim.x;
+            x[a] = v < nv ? __ldg(ur + v) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int c = 0; c < kDots; ++c) {
-            if (c < nc) {
-              float fy[8];
-              Vec<__nv_bfloat16>::load(y[c], fy);
+            for (int c = 0; c < kDots; ++c)
+              y[a][c] = v < nv && c < nc ? __ldg(er[c] + v) : make_uint4(0, 0, 0, 0);
+          }
 #pragma unroll
-              for (int k = 0; k < 8; ++k) acc[c] += (double)(fx[k] * fy[k]);
+          for (int a = 0; a < kAhead; ++a) {
+            float fx[8], fy[8];
+            Vec<__nv_bfloat16>::load(x[a], fx);
+#pragma unroll
+            for (int c = 0; c < kDots; ++c) {
+              if (c < nc) {
+                Vec<__nv_bfloat16>::load(y[a][c], fy);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[c] += (double)(fx[k] * fy[k]);
+              }
             }
           }
         }
@@ -743,12 +774,13 @@ int dispatch_v(int N) {
 }
 
 // Rows of partial logits over every token count up to T: slices times tokens
-// is at most the larger of T and what fills the pairs once (so a workspace for
-// more tokens serves fewer).
+// (whole groups of 32) is at most the larger of T and what fills the pairs once
+// (so a workspace for more tokens serves fewer).
 size_t slice_rows(int T, int n_et) {
-  const size_t fill = (size_t)kPairs * 2 * TM / n_et, most = (size_t)kMaxSlices * T;
+  const size_t t32 = (size_t)token_groups(T) * 32;
+  const size_t fill = (size_t)kPairs * 2 * TM / n_et, most = kMaxSlices * t32;
   const size_t rows = most < fill ? most : fill;
-  return rows > (size_t)T ? rows : (size_t)T;
+  return rows > t32 ? rows : t32;
 }
 size_t slice_rows64(int T, int N) {
   const size_t et = (N + kE64 - 1) / kE64, most = (size_t)kMaxSlices64 * T;
@@ -828,7 +860,9 @@ size_t route_scored_ws_bytes(int T, int d, int N_r) {
 
 // Tokens up to which the block path routes every token: a block per token
 // keeps a lone token's latency low, a warp per token costs a third of the
-// instructions.
+// instructions.  d 7168, 256 experts, softmax and grouped sigmoid: T 256 23 us
+// by blocks and 29 by warps, T 1024 36 and 42 against 38 and 42, and warps win
+// beyond.
 constexpr int kBlockTokens = 1024;
 
 namespace {

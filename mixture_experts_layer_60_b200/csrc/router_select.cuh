@@ -340,23 +340,35 @@ __device__ __forceinline__ void select_gates(const X (&x)[V], int my_e, X m, X z
 }
 
 // ---------------------------------------------------------------- by a block
-// Shared memory of the block path, for N experts and K slots.
+// Shared memory of the block path, for N experts, K slots and up to
+// max(256, N) threads.
 struct BlockRoute {
   double* x;          // [N] logits: exact, or float32 ones where exact_f is 0
-  uint32_t* ord;      // [N + 3] keys in order form (0: not eligible)
+  uint32_t* ord;      // [N] keys in order form
+  uint32_t* best;     // [warps][block_keep(K)] each warp's best eligible keys in order (0: none)
   float* top_key;     // [K + 1] keys in order, the best one left out last
   uint16_t* top_id;   // [K + 1] their experts
   uint16_t* list;     // [N] experts whose exact logit is wanted
   uint8_t* exact_f;   // [N]
 };
+// Keys of one warp that can be among the first K + 1, in whole vectors of four.
+__host__ __device__ __forceinline__ int block_keep(int K) {
+  return K + 1 < 32 ? (K + 4) / 4 * 4 : 32;
+}
+__host__ __device__ __forceinline__ int block_best(int N, int K) {
+  const int warps = N > 256 ? (N + 31) / 32 : 8;
+  return warps * block_keep(K);
+}
 __host__ __device__ inline size_t block_route_bytes(int N, int K) {
-  return (size_t)N * 8 + ((size_t)N + 4) * 4 + ((size_t)K + 2) * 8 + (size_t)N * 2 + N + 16;
+  return (size_t)N * 8 + 8 + ((size_t)N + 4) * 4 + (size_t)block_best(N, K) * 4 +
+         ((size_t)K + 2) * 8 + (size_t)N * 2 + N + 16;
 }
 __device__ __forceinline__ BlockRoute block_route_smem(uint8_t* p, int N, int K) {
   BlockRoute b;
   b.x = reinterpret_cast<double*>(p);
   b.ord = reinterpret_cast<uint32_t*>(p + (size_t)((N + 1) / 2 * 2) * 8);   // 16-byte aligned
-  b.top_key = reinterpret_cast<float*>(b.ord + (N + 3) / 4 * 4);
+  b.best = b.ord + (N + 3) / 4 * 4;                                         // 16-byte aligned
+  b.top_key = reinterpret_cast<float*>(b.best + block_best(N, K));
   b.top_id = reinterpret_cast<uint16_t*>(b.top_key + K + 1);
   b.list = b.top_id + K + 1;
   b.exact_f = reinterpret_cast<uint8_t*>(b.list + N);
@@ -440,11 +452,21 @@ __device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRul
     if (grouped) {
       // place inside the group; the first one or two make its score
       int place = 0;
-      if (mine)
+      if (mine && gs % 4 == 0) {
+        const uint4* row = reinterpret_cast<const uint4*>(b.ord) + g * (gs / 4);
+        const int at = e - g * gs;
+#pragma unroll 4
+        for (int i = 0; i < gs; i += 4) {
+          const uint4 v = row[i / 4];
+          place += (v.x > o || (v.x == o && i < at)) + (v.y > o || (v.y == o && i + 1 < at)) +
+                   (v.z > o || (v.z == o && i + 2 < at)) + (v.w > o || (v.w == o && i + 3 < at));
+        }
+      } else if (mine) {
         for (int i = g * gs; i < g * gs + gs; ++i) {
           const uint32_t v = b.ord[i];
           place += v > o || (v == o && i < e);
         }
+      }
       if (mine && place < 2) gkey[g][place] = key;
       __syncthreads();
       const float need = gkey[g][two ? 1 : 0];       // the last key the group's score counts
@@ -476,25 +498,33 @@ __device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRul
           !(last - next < 2.f * emax))
         z_open = true;
       if (mine && !((kept >> g) & 1u)) o = 0u;
-      __syncthreads();                               // every thread has read ord for its place
-      if (mine) b.ord[e] = o;
-      __syncthreads();
     }
-    // place in the order: how many eligible keys come before
+    // place in the order: how many eligible keys come before.  First inside the
+    // warp, whose best `keep` go into its row of b.best; only they can be among
+    // the first K + 1, and they count the other warps' rows.
+    const int warp = e >> 5, nw = blockDim.x >> 5;
     int place = 0;
-    if (mine && o != 0u) {
-      const uint4* ov = reinterpret_cast<const uint4*>(b.ord);
-      const int n4 = N / 4;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t v = __shfl_sync(0xffffffffu, o, i);
+      place += v > o || (v == o && i < lane);
+    }
+    const int keep = block_keep(K), n4 = keep / 4;
+    if (place < keep) b.best[warp * keep + place] = o;
+    __syncthreads();
+    if (o != 0u && place <= K) {
+      const uint4* row = reinterpret_cast<const uint4*>(b.best);
       int i = 0;
 #pragma unroll 4
-      for (; i < n4; ++i) {
-        const uint4 v = ov[i];
-        place += (v.x > o || (v.x == o && 4 * i < e)) + (v.y > o || (v.y == o && 4 * i + 1 < e)) +
-                 (v.z > o || (v.z == o && 4 * i + 2 < e)) + (v.w > o || (v.w == o && 4 * i + 3 < e));
+      for (; i < warp * n4; ++i) {                   // an equal key of a lower expert comes first
+        const uint4 v = row[i];
+        place += (v.x >= o) + (v.y >= o) + (v.z >= o) + (v.w >= o);
       }
-      for (int k = 4 * n4; k < N; ++k) {
-        const uint32_t v = b.ord[k];
-        place += v > o || (v == o && k < e);
+      i += n4;
+#pragma unroll 4
+      for (; i < nw * n4; ++i) {
+        const uint4 v = row[i];
+        place += (v.x > o) + (v.y > o) + (v.z > o) + (v.w > o);
       }
     }
     const bool placed = mine && o != 0u && place <= K;
