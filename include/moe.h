@@ -156,6 +156,8 @@ moe_status moe_route_grouped(const void* u, const void* E, moe_dtype dt, const f
  *                moe_balance_loss and moe_route_scored_backward
  *   workspace    device, >= moe_route_scored_workspace_size(T, d, N_r) bytes,
  *                256-byte aligned; nothing in it outlives the call
+ * Requires 1 <= K <= N_r <= 1024, T <= 2^30 and T * N_r < 2^31, d a multiple of
+ * 64 with rows of u of at most 32 KB.
  * ------------------------------------------------------------------------ */
 size_t moe_route_scored_workspace_size(int T, int d, int N_r);
 moe_status moe_route_scored(const void* u, const void* E, moe_dtype dt, const float* b, int T,
@@ -188,7 +190,8 @@ moe_status moe_route_scored(const void* u, const void* E, moe_dtype dt, const fl
  *   workspace   device, >= moe_balance_loss_workspace_size(T, N_r, n_seq)
  *               bytes, 256-byte aligned
  * Sums run in a fixed order: equal inputs give equal bits.
- * Requires 1 <= K <= N_r <= 1024, 1 <= n_seq <= 2^20.
+ * Requires 1 <= K <= N_r <= 1024, T <= 2^30 and T * N_r < 2^31,
+ * 1 <= n_seq <= 2^20.
  * ------------------------------------------------------------------------ */
 size_t moe_balance_loss_workspace_size(int T, int N_r, int n_seq);
 moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx,

@@ -405,14 +405,15 @@ def _want(who, **tensors):
             raise ValueError(f"{who}: {name} has shape {tuple(t.shape)}, not {shape}")
 
 
-def _here(who, t, stream):
+def _here(who, stream, *tensors):
     """The stream's handle (None: the current one of the current device).  The library launches on
-    the current device: the call's tensors have to live there."""
-    if not t.is_cuda:
+    the current device: all of the call's tensors (None: not given) have to live there."""
+    if not tensors[0].is_cuda:
         raise ValueError("libmoe takes device tensors only")
     dev = torch._C._cuda_getDevice()
-    if t.get_device() != dev:
-        raise ValueError(f"{who}: tensors are on {t.device}, not on the current device")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{who}: a tensor is on {t.device}, not on the current device")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _s(stream)
 
 
@@ -429,7 +430,7 @@ def moe_route_scored(u, E, b, K, topk_idx, topk_gate, counts, workspace,
     who = "moe_route_scored"
     T, d = u.shape
     N_r = E.shape[0]
-    st = _here(who, u, stream)
+    st = _here(who, stream, u, E, b, topk_idx, topk_gate, counts, logits, workspace)
     _want(who, E=(E, u.dtype, (N_r, d)), b=(b, _F32, (N_r,)), topk_idx=(topk_idx, _I32, (T, K)),
           topk_gate=(topk_gate, _F32, (T, K)), counts=(counts, _I32, (N_r,)),
           logits=(logits, _F32, (T, N_r)))
@@ -450,7 +451,7 @@ def moe_balance_loss(logits, topk_idx, alpha, loss, coef, workspace, score=MOE_S
     T, N_r = logits.shape
     n_seq = loss.shape[0]
     K = topk_idx.shape[1]
-    st = _here(who, logits, stream)
+    st = _here(who, stream, logits, topk_idx, loss, coef, seq_offsets, workspace)
     _want(who, logits=(logits, _F32, (T, N_r)), topk_idx=(topk_idx, _I32, (T, K)),
           loss=(loss, _F32, (n_seq,)), coef=(coef, _F32, (n_seq, N_r)),
           seq_offsets=(seq_offsets, _I32, (n_seq + 1,)))
@@ -475,7 +476,8 @@ def moe_route_scored_backward(u, E, logits, topk_idx, d_gate, du, dE, workspace,
     N_r = E.shape[0]
     K = topk_idx.shape[1]
     n_seq = 1 if balance_coef is None else balance_coef.shape[0]
-    st = _here(who, u, stream)
+    st = _here(who, stream, u, E, logits, topk_idx, d_gate, du, dE, seq_offsets, balance_coef,
+               d_loss, du_base, d_logit, workspace)
     _want(who, E=(E, u.dtype, (N_r, d)), logits=(logits, _F32, (T, N_r)),
           topk_idx=(topk_idx, _I32, (T, K)), d_gate=(d_gate, _F32, (T, K)),
           du=(du, u.dtype, (T, d)), dE=(dE, _F32, (N_r, d)), du_base=(du_base, u.dtype, (T, d)),
@@ -501,7 +503,7 @@ def moe_expert_gate_up_save8(x, offsets, W_gate_up, h, a_q, a_scale, stream=None
     who = "moe_expert_gate_up_save8"
     rows, d = x.shape
     n_groups, two_i, _ = W_gate_up.shape
-    st = _here(who, x, stream)
+    st = _here(who, stream, x, offsets, W_gate_up, h, a_q, a_scale)
     _want(who, W_gate_up=(W_gate_up, x.dtype, (n_groups, two_i, d)),
           offsets=(offsets, _I32, (n_groups + 1,)), h=(h, x.dtype, (rows, two_i // 2)),
           a_q=(a_q, _E4M3, (rows, two_i)), a_scale=(a_scale, _F32, (rows, two_i // 128)))
@@ -521,7 +523,8 @@ def moe_expert_ffn_backward8(x, offsets, W_gate_up, W_down, a_q, a_scale, dy, dx
     who = "moe_expert_ffn_backward8"
     rows, d = dy.shape
     n_groups, two_i, _ = W_gate_up.shape
-    st = _here(who, x, stream)
+    st = _here(who, stream, x, offsets, W_gate_up, W_down, a_q, a_scale, dy, dx, dW_gate_up,
+               dW_down, workspace)
     t = x.dtype
     _want(who, x=(x, t, (rows, d)), W_gate_up=(W_gate_up, t, (n_groups, two_i, d)),
           W_down=(W_down, t, (n_groups, d, two_i // 2)), offsets=(offsets, _I32, (n_groups + 1,)),

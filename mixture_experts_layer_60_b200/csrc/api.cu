@@ -198,8 +198,8 @@ moe_status check_scored(const char* who, int T, int N_r, int K, int score) {
               who, T, N_r, K);
   MOE_REQUIRE(N_r <= 1024 && K <= N_r, MOE_ERR_UNSUPPORTED,
               "%s: need 1 <= K <= N_r <= 1024 (K=%d N_r=%d)", who, K, N_r);
-  MOE_REQUIRE((long long)T * N_r <= 0x7fffffffLL, MOE_ERR_UNSUPPORTED,
-              "%s: T * N_r must fit in 31 bits (T=%d N_r=%d)", who, T, N_r);
+  MOE_REQUIRE((long long)T * N_r <= 0x7fffffffLL && T <= 1 << 30, MOE_ERR_UNSUPPORTED,
+              "%s: T * N_r must fit in 31 bits and T in 30 (T=%d N_r=%d)", who, T, N_r);
   MOE_REQUIRE(score == MOE_SCORE_SIGMOID || score == MOE_SCORE_SOFTMAX, MOE_ERR_INVALID_ARG,
               "%s: unknown score %d", who, score);
   return MOE_OK;

@@ -59,7 +59,9 @@ __device__ __forceinline__ int seq_at(const int32_t* off, int n_seq, int t) {
   return lo;
 }
 
-constexpr int kChunk = 64;       // tokens per block of the balance sums
+// Tokens per block of the balance sums (T 8192, 256 experts and T 50000, 61: 14
+// and 19 us; 128 tokens, fewer and longer blocks, 16 and 20).
+constexpr int kChunk = 64;
 
 // Partial sums of one (chunk of tokens, sequence) pair, row chunk + sequence:
 // along the pairs either number grows, so the rows are distinct.  Each of W
@@ -437,7 +439,8 @@ __global__ void __launch_bounds__(256) router_product_kernel(
     const float* base, float* C, int M, int N, int Kd) {
   __shared__ float sa[16][64 + 4], sb[16][64 + 4];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
+  const int n_n = (N + 63) / 64;               // tiles in one grid dimension: M may be many tokens
+  const int m0 = (int)(blockIdx.x / n_n) * 64, n0 = (int)(blockIdx.x % n_n) * 64;
   float acc[4][4] = {}, tot[4][4] = {};
   for (int k0 = 0; k0 < Kd; k0 += 16) {
     for (int i = tid; i < 16 * 64; i += 256) {
@@ -560,7 +563,7 @@ moe_status launch_route_scored_backward(const void* u, const void* E, moe_dtype 
   moe_status st = cuda_check(cudaGetLastError(), "router_logit_grad launch");
   if (st != MOE_OK) return st;
   if (tc) return launch_router_grad_tc(u, E, T, d, N_r, du_base, du, dE, ws, s);
-  const dim3 gu((d + 63) / 64, (T + 63) / 64), ge((d + 63) / 64, (N_r + 63) / 64);
+  const unsigned nd = (d + 63) / 64, gu = nd * ((T + 63) / 64), ge = nd * ((N_r + 63) / 64);
   router_product_kernel<false><<<gu, 256, 0, s>>>(dl, N_r, static_cast<const float*>(E), d,
                                                   static_cast<const float*>(du_base),
                                                   static_cast<float*>(du), T, d, N_r);

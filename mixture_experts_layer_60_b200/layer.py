@@ -247,7 +247,8 @@ class MoELayer:
         routed and shared experts for backward().  bf16 and FP8 layers.  With
         balance_alpha > 0, self.balance holds the balance loss of every
         sequence [seq_offsets[q], seq_offsets[q+1]) of the tokens (int32 on the
-        device; default: one sequence of all of them)."""
+        device; default: one sequence of all of them); without a balance loss
+        they are not looked at."""
         c = self.cfg
         if c.dtype not in ("bf16", "e4m3"):
             raise ValueError("the backward is implemented for bf16 and FP8 layers")

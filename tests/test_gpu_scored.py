@@ -465,3 +465,25 @@ def test_route_scored_backward_no_tokens():
     moe.moe_route_scored_backward(u, E, z, z[:, :4].int(), z[:, :4].contiguous(), u.clone(), dE,
                                   None)
     assert not dE.any()
+
+
+def test_route_scored_backward_float32_many_tokens():
+    """More 64-token tiles than a grid's second dimension holds."""
+    T, d, N, K = 65536 * 64 + 5, 64, 2, 1
+    g = torch.Generator(device="cuda").manual_seed(5)
+    u = torch.randn(T, d, generator=g, device="cuda")
+    E = torch.randn(N, d, generator=g, device="cuda")
+    logits = torch.randn(T, N, generator=g, device="cuda")
+    idx = torch.randint(0, N, (T, K), generator=g, device="cuda", dtype=torch.int32)
+    dg = torch.randn(T, K, generator=g, device="cuda")
+    du, dE, dl = torch.empty_like(u), torch.empty(N, d, device="cuda"), torch.empty_like(logits)
+    ws = torch.empty(max(1, moe.moe_route_scored_backward_workspace_size(moe.MOE_F32, T, d, N)),
+                     dtype=torch.uint8, device="cuda")
+    moe.moe_route_scored_backward(u, E, logits, idx, dg, du, dE, ws, renorm=False, d_logit=dl)
+    for rows in (slice(0, 64), slice(T - 69, T)):
+        a, e = dl[rows].double(), E.double()
+        # two products and a sum in float32, each off by at most half a step of
+        # the sum of the absolute values
+        bound = 3 * 2.0 ** -24 * (a.abs() @ e.abs())
+        assert ((du[rows].double() - a @ e).abs() <= bound).all()
+    assert torch.isfinite(dE).all()

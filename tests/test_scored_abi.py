@@ -177,3 +177,10 @@ def test_a_workspace_for_more_tokens_serves_fewer(L):
                      lambda T: L.moe_route_scored_backward_workspace_size(0, T, 7168, N)):
             at = [size(T) for T in list(range(1, 700, 13)) + list(range(700, 20500, 97))]
             assert all(a <= b for a, b in zip(at, at[1:]))
+
+
+def test_token_counts_past_the_index_range_are_refused(L):
+    T = (1 << 30) + 1                                      # T * N_r still fits in 31 bits
+    assert _route(L, T=T, N=1, K=1) == 2
+    assert L.moe_balance_loss(D, D, None, 1, T, 1, 1, 0, 1.0, D, D, D, BIG, None) == 2
+    assert b"moe_balance_loss" in L.moe_last_error()
