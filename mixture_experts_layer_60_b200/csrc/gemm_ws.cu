@@ -26,7 +26,7 @@
 //           before tiles were sized to the grid's rounds and divisions went by
 //           reciprocal and remainder); its epilogue is not under the products.
 //   DSWIGLU8  the SwiGLU backward from such a checkpoint; writes h again too
-//           (the down projection's weight gradient needs it).  Same rows: 151
+//           (the down projection's weight gradient needs it).  Same rows: 146
 //           us; 194 before the checkpoint's pieces were read under the products.
 // Values are transposed through a 2 KB shared-memory patch per warp so that
 // global stores are 16-byte vectors along token rows.
@@ -60,6 +60,13 @@ constexpr int STAGES = 3;
 constexpr int kEpiWarps = 8;        // two warps per TMEM lane quarter, alternating token chunks
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kMaxGroups = 1024;
+// Token tiles of 256, 224, ... 64 rows that the 8-bit checkpoint epilogues
+// choose from: one for each epilogue warp but the first.
+constexpr int kTileSizes = (TMAX - 64) / 32 + 1;
+static_assert(kTileSizes == kEpiWarps - 1, "a warp for each token tile size");
+__device__ __forceinline__ void epilogue_warps_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+}
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint32_t TMEM_COLS = 512;
 
@@ -76,6 +83,7 @@ constexpr int OFF_AMAX = OFF_TAB + 2 * (kMaxGroups + 1) * 4;
 // SWIGLU_SAVE8: [2 chunk halves][2 slots][4 lane quarters][gate, up][32 tokens] maxima
 // and a barrier for each (half, slot)
 constexpr int AMAX_BYTES = 2 * 2 * 4 * 2 * 32 * 4;
+static_assert(OFF_AMAX % 8 == 0, "the costs of the token tiles lie there first");
 constexpr int OFF_XBAR = (OFF_AMAX + AMAX_BYTES + 7) / 8 * 8;
 constexpr int OFF_TMAX = OFF_XBAR + 4 * 8;
 constexpr int SMEM_BYTES = OFF_TMAX + 8;
@@ -237,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* amax_x = reinterpret_cast<float*>(smem + OFF_AMAX);
   uint64_t* xbar = reinterpret_cast<uint64_t*>(smem + OFF_XBAR);
   int* s_tmax = reinterpret_cast<int*>(smem + OFF_TMAX);
+  long long* costs = reinterpret_cast<long long*>(smem + OFF_AMAX);   // before the first tile
   int* prefix = reinterpret_cast<int*>(smem + OFF_TAB);
   int* roff = prefix + kMaxGroups + 1;
 
@@ -268,38 +277,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
+  if (TileMath<EPI>::CHECK8 && warp >= 2) {
+    // The tokens per tile that finish first, each size weighed by a warp of its
+    // own (one warp after the other took 3 us): rounds of the grid times the
+    // cycles of a tile, which are the larger of its products (4 n a K step of
+    // 64) and of its operands through L2 (512 + 2 n), and an epilogue that
+    // nothing overlaps.  152 tiles of 256 on 148 SMs take two rounds; smaller
+    // tiles cost more per token but waste no second round.
+    if (warp == 2) load_offsets_warp(p.offsets, G, p.rows, roff, p.err);
+    epilogue_warps_sync();
+    if (warp > 2) {
+      const int n = TMAX - 32 * (warp - 3);
+      int tiles = 0;
+      for (int i = lane; i < Gtot; i += 32) {
+        int base, m, n_t, step;
+        group_span(i, G, roff, p, base, m);
+        token_tiling(m, n_t, step, n);
+        tiles += n_t * n_wt;
+      }
+      tiles = __reduce_add_sync(0xffffffffu, tiles);
+      const long long rounds = (tiles + gridDim.x - 1) / gridDim.x;
+      if (lane == 0)
+        costs[warp - 3] = rounds * ((long long)(p.K / BK) * max(4 * n, 512 + 2 * n) + 48 * n);
+    }
+    epilogue_warps_sync();
+  }
   if (warp == 2) {
     // Tile table: prefix[g] = first tile of group g; tiles of a group are
     // ordered weight-tile major, token-tile fastest.  Offsets are clamped
     // into disjoint ranges of [0, rows) first.
-    load_offsets_warp(p.offsets, G, p.rows, roff, p.err);
+    if (!TileMath<EPI>::CHECK8) load_offsets_warp(p.offsets, G, p.rows, roff, p.err);
     const int per = (Gtot + 31) / 32;
     const int g0 = lane * per;
     int tmax = TMAX;
     if (TileMath<EPI>::CHECK8) {
-      // The tokens per tile that finish first: rounds of the grid times the
-      // cycles of a tile, which are the larger of its products (4 n a K step
-      // of 64) and of its operands through L2 (512 + 2 n), and an epilogue
-      // that nothing overlaps.  152 tiles of 256 on 148 SMs take two rounds;
-      // smaller tiles cost more per token but waste no second round.
-      long long best = -1;
-      for (int n = TMAX; n >= 64; n -= 32) {
-        int tiles = 0;
-        for (int i = 0; i < per; ++i)
-          if (g0 + i < Gtot) {
-            int base, m, n_t, step;
-            group_span(g0 + i, G, roff, p, base, m);
-            token_tiling(m, n_t, step, n);
-            tiles += n_t * n_wt;
-          }
-        tiles = __reduce_add_sync(0xffffffffu, tiles);
-        const long long rounds = (tiles + gridDim.x - 1) / gridDim.x;
-        const long long cost = rounds * ((long long)(p.K / BK) * max(4 * n, 512 + 2 * n) + 48 * n);
-        if (best < 0 || cost < best) {
-          best = cost;
-          tmax = n;
+      long long best = costs[0];
+      for (int i = 1; i < kTileSizes; ++i)
+        if (costs[i] < best) {
+          best = costs[i];
+          tmax = TMAX - 32 * i;
         }
-      }
       if (lane == 0) *s_tmax = tmax;
     }
     int local = 0;
