@@ -487,3 +487,47 @@ def test_route_scored_backward_float32_many_tokens():
         bound = 3 * 2.0 ** -24 * (a.abs() @ e.abs())
         assert ((du[rows].double() - a @ e).abs() <= bound).all()
     assert torch.isfinite(dE).all()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,N,K,kw", [
+    *[(20, 96, K, {}) for K in (1, 3, 4, 27, 28, 30, 31, 32, 33, 64, 95, 96)],
+    (40, 66, 5, dict(n_groups=6, topk_groups=3, group_top=2)),       # groups of 11
+    (40, 66, 22, dict(n_groups=3, topk_groups=1)),                   # as many as the group holds
+    (40, 64, 3, dict(n_groups=32, topk_groups=2, group_top=2)),      # groups of two
+    (2000, 66, 5, dict(n_groups=6, topk_groups=3, group_top=2)),
+    (12, 1024, 1024, {}),
+    (1100, 1024, 33, {}),
+])
+def test_route_scored_ranks_across_warps(dt, T, N, K, kw):
+    """Slots around a warp's 32 keys, group sizes of no vector, the largest sizes."""
+    u, E, b = _inputs(T, 128, N, dt, 900 + K + N)
+    for score in (SIG, SOFT):
+        _check_route(u, E, b, K, score, **kw)
+
+
+@pytest.mark.parametrize("T", [6, 100, 1500])
+def test_route_scored_equal_keys_across_warps(T):
+    """Four distinct experts, each in every warp many times over: ties go by index."""
+    u, E, _ = _inputs(T, 192, 256, torch.bfloat16, 12)
+    E = E[torch.arange(256, device="cuda") % 4].contiguous()
+    for kw in (dict(), dict(n_groups=8, topk_groups=3, group_top=2)):
+        _check_route(u, E, None, 40, SIG, **kw)
+        _check_route(u, E, None, 40, SOFT, renorm=False, **kw)
+
+
+def test_route_scored_calls_at_once():
+    """Calls on two streams, each with its own buffers, are those of one stream."""
+    cases = [(_inputs(T, 512, 128, torch.bfloat16, 40 + T), score) for T, score in
+             ((200, SIG), (1800, SOFT))]
+    alone = [_route(*i[:2], i[2], 6, score=s) for i, s in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(20):
+        both = []
+        for (i, s), st in zip(cases, streams):
+            with torch.cuda.stream(st):
+                both.append(_route(*i[:2], i[2], 6, score=s))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            assert all(torch.equal(x, y) for x, y in zip(a[:4], b[:4]))
