@@ -42,10 +42,31 @@ __device__ __forceinline__ void sigmoid_pair(float x, float& s, float& om) {
   om = x < 0.f ? inv : e * inv;
 }
 
+// A token whose sigmoids sum to less than this has every logit below -69: its s'
+// are formed from e^(x - xm), xm its largest logit, which is s(x) / s(xm) to a
+// part in e^69 and never underflows as a whole (1 / z would be infinite below
+// 2^-128).
+constexpr float kSmallSum = 1e-30f;
+
 // Row [r0, r1) of sequence q, made safe: inside [0, T], not negative.
 __device__ __forceinline__ void seq_range(const int32_t* off, int q, int T, int* err, int& r0,
                                           int& r1) {
   clamp_group_rows(off, q, T, err, r0, r1);
+}
+
+// Logits x of a token (a lane's V of them; -inf: none) to e^(x - xm); their sum.
+template <int V>
+__device__ __forceinline__ float relative_scores(float (&x)[V]) {
+  float m = -INFINITY, z = 0.f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) m = fmaxf(m, x[j]);
+  m = wmax(m);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    x[j] = expf(x[j] - m);
+    z += x[j];
+  }
+  return wsum(z);
 }
 
 // The last sequence whose first token is <= t (-1: t lies before the first).
@@ -145,6 +166,16 @@ __global__ void __launch_bounds__(32 * W) balance_partial_kernel(
       }
 #pragma unroll
       for (int c = 0; c < U; ++c) z[c] = wsum(z[c]);
+      if (!softmax) {
+#pragma unroll
+        for (int c = 0; c < U; ++c) {
+          if (tb + c >= r1 || !(z[c] < kSmallSum)) continue;
+          const float* row = logits + (size_t)(tb + c) * N;
+#pragma unroll
+          for (int j = 0; j < V; ++j) s[c][j] = j * 32 + lane < N ? row[j * 32 + lane] : -INFINITY;
+          z[c] = relative_scores(s[c]);
+        }
+      }
 #pragma unroll
       for (int c = 0; c < U; ++c) {
         const float inv = tb + c < r1 ? 1.f / z[c] : 0.f;
@@ -290,7 +321,18 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_logit_grad_kernel(
         om[j] = 0.f;
       }
     }
-    const float inv = 1.f / wsum(z);
+    z = wsum(z);
+    if (!softmax && z < kSmallSum) {
+      // s (1 - s) / sum s is e^(x - xm) / sum e^(x - xm) here, and 1 - s is 1
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int e = expert(j);
+        s[j] = e < N ? lrow[e] : -INFINITY;
+        om[j] = 1.f;
+      }
+      z = relative_scores(s);
+    }
+    const float inv = 1.f / z;
     if (softmax) {
 #pragma unroll
       for (int j = 0; j < V; ++j) s[j] *= inv;

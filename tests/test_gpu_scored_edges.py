@@ -1,0 +1,92 @@
+"""The scored router, its balance loss and gradients where float32 sums cancel, underflow or tie.
+
+Tolerances are counted from the arithmetic before any run:
+  selection   exact, against float64 logits
+  loss        sums of s' of at most 16 float32 roundings: 2^-20
+  d_logit     2^-20 (2 scale sum|d_gate| + 2 max|q|); where a token's renormalised gates
+              have no gradient (one slot, or equal upstream values) only the balance
+              term's share is left: 2^-20 * 2 max|q|
+"""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_60_b200 as moe
+from oracle import moe_scored as S
+from tests.harness import f64
+
+pytestmark = pytest.mark.gpu
+
+SIG, SOFT = moe.MOE_SCORE_SIGMOID, moe.MOE_SCORE_SOFTMAX
+BF = torch.bfloat16
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _normal(T, d, N, seed, dt=BF):
+    g = _gen(seed)
+    u = torch.randn(T, d, generator=g, device="cuda").to(dt)
+    E = (torch.randn(N, d, generator=g, device="cuda") * d ** -0.5).to(dt)
+    b = (torch.rand(N, generator=g, device="cuda") * 2 - 1) * 0.01
+    return u, E, b
+
+
+# ------------------------------------------------------------------ underflow
+
+def _underflow(T, N, K, seed, rows):
+    """Logits of which the given rows lie far below every float32 sigmoid."""
+    g = _gen(seed)
+    x = torch.randn(T, N, generator=g, device="cuda")
+    low = -90 - 210 * torch.rand(len(rows), 1, generator=g, device="cuda")
+    x[rows] = low + 3 * torch.randn(len(rows), N, generator=g, device="cuda")
+    return x, torch.topk(x, K, dim=1).indices.int(), g
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,N,K,rows", [(70, 32, 4, [3]), (9, 256, 8, list(range(9))),
+                                        (130, 61, 6, [0, 64, 129])])
+def test_backward_of_underflowing_sigmoids(renorm, T, N, K, rows):
+    d = 128
+    x, idx, g = _underflow(T, N, K, 5, rows)
+    dg = torch.randn(T, K, generator=g, device="cuda") * 0.1
+    coef = torch.rand(1, N, generator=g, device="cuda") * 0.01
+    for dt in (BF, torch.float32):
+        u, E, _ = _normal(T, d, N, 6, dt)
+        for dgx, cx in ((dg, None), (dg, coef), (None, coef)):
+            du = torch.full((T, d), float("nan"), dtype=dt, device="cuda")
+            dE = torch.full((N, d), float("nan"), device="cuda")
+            dl = torch.full((T, N), float("nan"), device="cuda")
+            ws = torch.empty(moe.moe_route_scored_backward_workspace_size(
+                moe.MOE_BF16 if dt == BF else moe.MOE_F32, T, d, N), dtype=torch.uint8,
+                device="cuda")
+            moe.moe_route_scored_backward(u, E, x, idx, dgx, du, dE, ws, score=SIG, renorm=renorm,
+                                          gate_scale=2.5, balance_coef=cx, d_logit=dl)
+            want = S.backward(f64(x), idx.cpu().numpy(), None if dgx is None else f64(dgx),
+                              [0, T], None if cx is None else f64(cx), None, S.SIGMOID, renorm, 2.5)
+            mag = np.zeros((T, 1))
+            if dgx is not None:
+                mag = mag + 2 * 2.5 * np.abs(f64(dgx)).sum(1, keepdims=True)
+            if cx is not None:
+                mag = mag + 2 * f64(cx).max()
+            assert torch.isfinite(dl).all() and torch.isfinite(du).all() and torch.isfinite(dE).all()
+            assert (np.abs(f64(dl) - want) <= 2.0 ** -20 * mag).all()
+
+
+@pytest.mark.parametrize("T,N,K,off", [(300, 61, 6, None), (1000, 256, 8, [0, 10, 10, 700, 990]),
+                                       (70, 600, 5, [0, 70])])
+def test_balance_of_underflowing_sigmoids(T, N, K, off):
+    x, idx, _ = _underflow(T, N, K, 7, [0, 9, 10, 69])
+    o = [0, T] if off is None else off
+    ot = None if off is None else torch.tensor(off, dtype=torch.int32, device="cuda")
+    n = len(o) - 1
+    loss = torch.full((n,), float("nan"), device="cuda")
+    coef = torch.full((n, N), float("nan"), device="cuda")
+    ws = torch.empty(moe.moe_balance_loss_workspace_size(T, N, n), dtype=torch.uint8, device="cuda")
+    moe.moe_balance_loss(x, idx, 1e-3, loss, coef, ws, score=SIG, seq_offsets=ot)
+    wl, wc = S.balance(f64(x), idx.cpu().numpy(), o, 1e-3, S.SIGMOID)
+    assert (np.abs(f64(coef) - wc) <= 2.0 ** -23 * np.abs(wc)).all()
+    assert (np.abs(f64(loss) - wl) <= 2.0 ** -20 * np.abs(wl)).all()
