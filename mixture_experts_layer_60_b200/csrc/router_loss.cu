@@ -13,6 +13,9 @@
 //   sigmoid: s_i (1 - s_i) (q_i - Q) / sum_j s_j + sum over slots k of i of
 //            s_i (1 - s_i) scale dg_k  (raw)
 //            g~_k (1 - s_i) (scale dg_k - G)  (renormalised)
+// Renormalised gates sum to a constant, so only differences of dg_k matter: dg_k
+// and G are taken relative to the dg of the token's first slot, and upstream
+// values that are equal (or a single slot's) leave exactly the balance term.
 #include <math.h>
 
 #include "launch.h"
@@ -367,7 +370,8 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_logit_grad_kernel(
       };
       int e = -1;
       float dg = 0.f, x = -INFINITY, xm = -INFINITY, sxm = 1.f, den = 1.f, G = 0.f, dum;
-      bool ratio = false;
+      float dg0 = 0.f;                                     // dg of the first slot that counts
+      bool ratio = false, first = true;
       const auto weight = [&](float v) {                   // the score over the largest one
         if (!ratio) return expf(v - xm);
         float a, b;
@@ -378,6 +382,11 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_logit_grad_kernel(
         for (int k0 = 0; k0 < K; k0 += 32) {
           slot(k0 + lane, e, dg, x);
           if (e >= 0) xm = x > xm || x != x ? x : xm;
+          const unsigned counts = __ballot_sync(0xffffffffu, e >= 0);
+          if (first && counts) {
+            dg0 = __shfl_sync(0xffffffffu, dg, __ffs(counts) - 1);
+            first = false;
+          }
         }
         xm = wmax(xm);
         ratio = !softmax && !(xm < -30.f);
@@ -388,7 +397,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_logit_grad_kernel(
           if (e >= 0) {
             const float v = weight(x);
             w += v;
-            wd = fmaf(v, dg, wd);
+            wd = fmaf(v, dg - dg0, wd);
           }
         }
         den = wsum(w);
@@ -401,7 +410,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_logit_grad_kernel(
           float a, b;
           if (softmax) { a = expf(x - m) * inv; b = 1.f; }
           else sigmoid_pair(x, a, b);
-          if (renorm) v = weight(x) / den * b * (dg - G);
+          if (renorm) v = weight(x) / den * b * (dg - dg0 - G);
           else { v = a * b * dg; R += softmax ? v : 0.f; }
         }
         __syncwarp();

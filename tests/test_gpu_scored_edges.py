@@ -90,3 +90,28 @@ def test_balance_of_underflowing_sigmoids(T, N, K, off):
     wl, wc = S.balance(f64(x), idx.cpu().numpy(), o, 1e-3, S.SIGMOID)
     assert (np.abs(f64(coef) - wc) <= 2.0 ** -23 * np.abs(wc)).all()
     assert (np.abs(f64(loss) - wl) <= 2.0 ** -20 * np.abs(wl)).all()
+
+
+# ------------------------------------------------------------------ gradients that cancel
+
+@pytest.mark.parametrize("score", [SIG, SOFT])
+@pytest.mark.parametrize("T,N,K", [(1, 8, 1), (100, 300, 1), (1500, 64, 1), (64, 64, 2),
+                                   (300, 96, 8), (33, 64, 40)])
+def test_equal_gate_gradients_leave_the_balance_term_alone(score, T, N, K):
+    """Renormalised gates sum to a constant: upstream values that are the same for all of a
+    token's slots have no gradient, and one slot never has."""
+    d = 64
+    u, E, _ = _normal(T, d, N, 30 + T)
+    g = _gen(31 + K)
+    x = torch.randn(T, N, generator=g, device="cuda")
+    idx = torch.topk(x, K, dim=1).indices.int()
+    dg = torch.randn(T, 1, generator=g, device="cuda").expand(T, K).contiguous()
+    coef = 0.01 * torch.rand(1, N, generator=g, device="cuda") / T
+    du, dE = torch.empty_like(u), torch.empty(N, d, device="cuda")
+    dl = torch.full((T, N), float("nan"), device="cuda")
+    ws = torch.empty(moe.moe_route_scored_backward_workspace_size(moe.MOE_BF16, T, d, N),
+                     dtype=torch.uint8, device="cuda")
+    moe.moe_route_scored_backward(u, E, x, idx, dg, du, dE, ws, score=score, renorm=True,
+                                  gate_scale=2.5, balance_coef=coef, d_logit=dl)
+    want = S.backward(f64(x), idx.cpu().numpy(), None, [0, T], f64(coef), None, score, True, 2.5)
+    assert (np.abs(f64(dl) - want) <= 2.0 ** -20 * 2 * f64(coef).max()).all()
