@@ -155,6 +155,13 @@ struct Selection {
   uint32_t mask;
 };
 
+// The sizes at which a group's keys and their sum are rounded (a sum may be far
+// smaller than its keys); 0 where one is infinite: no rounding moves that score.
+__device__ __forceinline__ float group_rounding(float a, float b) {
+  const float v = fabsf(a) + fabsf(b) + fabsf(a + b);
+  return v < INFINITY ? v : 0.f;
+}
+
 // Whether an expert with this key can take part in the open decisions.
 __device__ __forceinline__ bool takes_part(float key, float lo, float hi, float err) {
   const float pad = 3.f * err + 2.f * kKeyRounding * fabsf(key);
@@ -219,7 +226,14 @@ __device__ __forceinline__ Selection select_core(const float (&key)[V], float er
       __syncwarp();
     }
     uint32_t go = 0u;
-    if (lane < r.n_groups) go = sel_ord(two ? sel_val(ga) + sel_val(gb) : sel_val(ga));
+    float gm = 0.f;
+    if (lane < r.n_groups) {
+      const float ka = sel_val(ga), kb = two ? sel_val(gb) : 0.f;
+      go = sel_ord(two ? ka + kb : ka);
+      gm = group_rounding(ka, kb);
+    }
+    // what rounding the keys and their sum moves a group's score by
+    const float grel = rel * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(gm)));
     unsigned kept = 0;
     float last = INFINITY, next = 0.f;
     const float gsc = lane < r.n_groups ? sel_val(go) : NAN;
@@ -233,12 +247,12 @@ __device__ __forceinline__ Selection select_core(const float (&key)[V], float er
         last = next;
         if (lane == bg) go = 0u;
       } else {
-        out.open = last - next < 2.f * r.group_top * err + rel * (fabsf(last) + fabsf(next));
+        out.open = last - next < 2.f * (r.group_top * err + grel);
       }
     }
     if (out.open) {
       // the members that can enter the scores of the groups near the border
-      const float room = 4.f * r.group_top * err + 2.f * rel * (fabsf(last) + fabsf(next));
+      const float room = 4.f * (r.group_top * err + grel);
       const float need = gsc >= next - room && gsc <= last + room ? sel_val(two ? gb : ga) : INFINITY;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -477,7 +491,9 @@ __device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRul
       const bool has = lane < r.n_groups;
       const float gsc = has ? (two ? gkey[lane][0] + gkey[lane][1] : gkey[lane][0]) : 0.f;
       const uint32_t go = has ? sel_ord(gsc) : 0u;
-      const float ge = has && ((s_near >> lane) & 1u) ? r.group_top * err + rel * fabsf(gsc) : 0.f;
+      const float ge = has && ((s_near >> lane) & 1u)
+                           ? r.group_top * err + rel * group_rounding(gkey[lane][0], two ? gkey[lane][1] : 0.f)
+                           : 0.f;
       int before = 0;
       for (int q = 0; q < r.n_groups; ++q) {
         const uint32_t v = __shfl_sync(0xffffffffu, go, q);

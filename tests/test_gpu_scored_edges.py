@@ -35,6 +35,32 @@ def _normal(T, d, N, seed, dt=BF):
     return u, E, b
 
 
+def _route(u, E, b, K, **kw):
+    T, d = u.shape
+    N = E.shape[0]
+    idx = torch.full((T, K), -7, dtype=torch.int32, device="cuda")
+    gate = torch.full((T, K), float("nan"), device="cuda")
+    counts = torch.full((N,), 12345, dtype=torch.int32, device="cuda")
+    ws = torch.full((max(256, moe.moe_route_scored_workspace_size(T, d, N)),), 255,
+                    dtype=torch.uint8, device="cuda")
+    moe.moe_route_scored(u, E, b, K, idx, gate, counts, ws, **kw)
+    return idx, gate, counts
+
+
+def _check_selection(u, E, b, K, score, n_groups=1, topk_groups=1, group_top=1, **kw):
+    idx, gate, counts = _route(u, E, b, K, score=score, n_groups=n_groups,
+                               topk_groups=topk_groups, group_top=group_top, **kw)
+    x = f64(u) @ f64(E).T
+    want = S.select(S.keys(x, None if b is None else b.cpu().numpy(), score), K, n_groups,
+                    topk_groups, group_top)
+    got = idx.cpu().numpy()
+    bad = (got != want).any(axis=1)
+    assert not bad.any(), f"{bad.sum()} of {len(bad)} tokens, first {np.nonzero(bad)[0][0]}: " \
+        f"{got[bad][0]} != {want[bad][0]}"
+    assert np.array_equal(counts.cpu().numpy(), np.bincount(want.reshape(-1), minlength=len(E)))
+    assert torch.isfinite(gate).all()
+
+
 # ------------------------------------------------------------------ underflow
 
 def _underflow(T, N, K, seed, rows):
@@ -115,3 +141,37 @@ def test_equal_gate_gradients_leave_the_balance_term_alone(score, T, N, K):
                                   gate_scale=2.5, balance_coef=coef, d_logit=dl)
     want = S.backward(f64(x), idx.cpu().numpy(), None, [0, T], f64(coef), None, score, True, 2.5)
     assert (np.abs(f64(dl) - want) <= 2.0 ** -20 * 2 * f64(coef).max()).all()
+
+
+# ------------------------------------------------------------------ groups
+
+@pytest.mark.parametrize("T", [1000, 1300])
+def test_groups_of_large_biases_that_cancel(T):
+    """A group's two keys near 8000 and -8000: a step of a key is 2^-11, a hundred times a
+    logit's error.  Where the float32 logit puts a key on the other side of a rounding than the
+    exact one, two groups that tie do not seem to."""
+    N, G, d = 64, 32, 7168
+    u, E, _ = _normal(T, d, N, 800)
+    lg = torch.empty(T, N, device="cuda")
+    _route(u, E, None, 8, logits=lg)
+    x = f64(u) @ f64(E).T
+    base = np.where(np.arange(N) % 2 == 0, 8000.0, -8000.0).astype(np.float32)
+    exact, seen = S.keys(x, base, S.SIGMOID), S.keys(f64(lg), base, S.SIGMOID)
+    found = np.argwhere(exact != seen)
+    assert len(found) >= 3
+    for t, e in found[:12]:
+        a = e // 2
+        up = seen[t, e] > exact[t, e]
+        if a == (0 if up else G - 1):
+            continue
+        c = (a - 1 if up else a + 1)               # ties keep the lower group
+        others = [g for g in range(G) if g not in (a, c)]
+        b = base.copy()
+        for k, g in enumerate(others):
+            b[2 * g] += 100 if k < 15 else -100    # surely kept, surely not
+        score = exact[t].reshape(G, 2).sum(1)
+        b[2 * c] += score[a] - score[c]            # a whole number of steps: now they tie
+        bt = torch.from_numpy(b).cuda()
+        idx, _, _ = _route(u, E, bt, 16, n_groups=G, topk_groups=16, group_top=2)
+        want = S.select(S.keys(x[t:t + 1], b, S.SIGMOID), 16, G, 16, 2)[0]
+        assert np.array_equal(idx[t].cpu().numpy(), want), (t, e, a, c)
