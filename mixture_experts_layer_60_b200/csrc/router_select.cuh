@@ -499,20 +499,25 @@ __device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRul
         const uint32_t v = __shfl_sync(0xffffffffu, go, q);
         before += v > go || (v == go && q < lane);
       }
-      const unsigned kept = __ballot_sync(0xffffffffu, has && before < r.topk_groups);
-      const int at_last = __ffs(__ballot_sync(0xffffffffu, has && before == r.topk_groups - 1)) - 1;
-      const int at_next = __ffs(__ballot_sync(0xffffffffu, has && before == r.topk_groups)) - 1;
-      const float last = __shfl_sync(0xffffffffu, gsc, at_last);
-      const float next = __shfl_sync(0xffffffffu, gsc, at_next);
-      const float emax = sel_warp_max(ge);
-      if (last - next < 2.f * emax) {
-        // the members that can enter the scores of the groups near the border
+      const bool keep = has && before < r.topk_groups;
+      const unsigned kept = __ballot_sync(0xffffffffu, keep);
+      // The choice is open where a kept group's score may lie below that of one
+      // left out; the inexact members of the groups that can be either are wanted.
+      // (NaN scores are exact and come first: they open nothing.)
+      const bool number = has && gsc == gsc;
+      const float least = -sel_warp_max(number && keep ? ge - gsc : -INFINITY);
+      const float most = sel_warp_max(number && !keep ? gsc + ge : -INFINITY);
+      if (least < most) {
         const float mine_sc = two ? gkey[g][0] + gkey[g][1] : gkey[g][0];
-        want = near && mine_sc >= next - 4.f * emax && mine_sc <= last + 4.f * emax;
+        const float mine_ge = __shfl_sync(0xffffffffu, ge, g);
+        want = near && (((kept >> g) & 1u) ? mine_sc - mine_ge < most : mine_sc + mine_ge > least);
+      } else if (eta > 0.f) {
+        // Scores that no member's error joins: the error of the softmax's sum, which a
+        // bias lets tell groups apart, and the keys' roundings may still.
+        const float gr = sel_warp_max(has ? group_rounding(gkey[lane][0], two ? gkey[lane][1] : 0.f) : 0.f);
+        const float ze = 2.f * kKeyRounding * gr + (bias ? 2.f * r.group_top * eta * smax : 0.f);
+        z_open = least - most <= ze;
       }
-      if (eta > 0.f && last - next <= 4.f * eta * smax + 2.f * kKeyRounding * fabsf(last) &&
-          !(last - next < 2.f * emax))
-        z_open = true;
       if (mine && !((kept >> g) & 1u)) o = 0u;
     }
     // place in the order: how many eligible keys come before.  First inside the

@@ -145,6 +145,55 @@ def test_equal_gate_gradients_leave_the_balance_term_alone(score, T, N, K):
 
 # ------------------------------------------------------------------ groups
 
+@pytest.mark.parametrize("T", [64, 1300])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_softmax_group_scores_a_rounding_apart(T, group_top):
+    """Copies of one token; the bias of one group is moved, a step of its key at a time, over the
+    point where the group choice turns.  Other groups keep inexact keys near their best."""
+    d, N, G, K = 7168, 32, 4, 2
+    for seed in range(8):
+        u, E, _ = _normal(1, d, N, 700 + seed)
+        u = (u.float() * 3).to(BF)                             # scores of some tenths
+        x = f64(u) @ f64(E).T
+        s = S.scores(x, S.SOFTMAX).astype(np.float32)
+        top = np.sort(s.reshape(G, -1), axis=1)[:, ::-1][:, :group_top].astype(np.float64)
+        b = np.zeros(N, np.float32)
+        b[0] = 4                                               # group 0 is always kept,
+        b[8:24] = 1                                            # then group 1 or group 2
+        # where their scores are equal, spread over the group's biases
+        diff = (top[1].sum() - top[2].sum()) / group_top
+        tokens = u.expand(T, d).contiguous()
+        step = 2.0 ** -23
+        for k in range(-8, 9):
+            b[16:24] = np.float32(round((1.0 + diff) / step) * step) + np.float32(k * step)
+            _check_selection(tokens, E, torch.from_numpy(b).cuda(), K, SOFT, n_groups=G,
+                             topk_groups=2, group_top=group_top)
+
+
+@pytest.mark.parametrize("T", [60, 1200])
+@pytest.mark.parametrize("score", [SIG, SOFT])
+def test_groups_beside_a_group_of_nan_or_infinite_keys(T, score):
+    """A group that always comes first or last, by a bias of NaN or +-inf, leaves the choice
+    among the others what it is."""
+    N, G, K = 64, 8, 8
+    u, E, b = _normal(T, 2048, N, 29)
+    E[24:32] = E[8:16]                             # groups 1 and 3 tie for every token
+    b[24:32] = b[8:16]
+    clean = b.clone()
+    x = f64(u) @ f64(E).T
+    for group, value in ((0, float("nan")), (0, float("inf")), (5, -float("inf"))):
+        b = clean.clone()
+        b[group * 8 + 3] = value
+        if value < 0:
+            b[group * 8:group * 8 + 8] = value
+        idx, _, _ = _route(u, E, b, K, score=score, n_groups=G, topk_groups=4, group_top=1)
+        key = S.keys(x, b.cpu().numpy(), score)
+        if value != value:
+            key[:, group * 8 + 3] = np.inf         # NaN comes first
+        want = S.select(key, K, G, 4, 1)
+        assert np.array_equal(idx.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("T", [1000, 1300])
 def test_groups_of_large_biases_that_cancel(T):
     """A group's two keys near 8000 and -8000: a step of a key is 2^-11, a hundred times a
