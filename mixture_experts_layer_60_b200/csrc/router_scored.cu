@@ -31,34 +31,44 @@ using namespace sm100;
 // A CTA pair (cta_group::2) owns 256 tokens x Nt <= 256 experts x one slice of
 // d: each CTA stages its 128 token rows (the MMA's M side) and half of the
 // experts, so the pair streams each centroid byte once.  The token side is
-// read once from memory.  T 8192, d 7168, 256 experts: 32 us, u at 3.7 TB/s.
+// read once from memory.  T 8192, d 7168, 256 experts: 41 us, u at 2.9 TB/s.
 // Some 9 us of it are there at any size (TMEM and barriers 1, first loads 1.5
 // to 2.5, last products and drain 1.5, stores 3, exit 1); the rest grows by 640
 // cycles a block of 64 columns, which is u's copy by the 64 pairs that 32
 // tiles of tokens in two slices keep busy.
 //
-// The tensor core adds into its accumulator with truncation: over the whole
-// of d = 7168 that biases a logit by some 3e-6 of its size.  The sum is
-// therefore cut every kChunk blocks of 64 (32 accumulation steps): two TMEM
-// buffers take turns, and the epilogue warps add each finished chunk into
-// float32 registers (round to nearest) while the next one runs.
+// The tensor core adds into its accumulator with truncation, and what a step
+// loses follows the largest of its products and running sums, not the logit.
+// The sum is therefore cut every kChunk blocks (16 accumulation steps): two TMEM
+// buffers take turns, and the epilogue warps add each finished chunk into float32
+// registers (round to nearest) while the next one runs.  A buffer's round trip
+// through the pair's barriers is some 4000 cycles, so shorter chunks stall the
+// products: chunks of 2, 4, 6 and 8 blocks take 52, 41, 39 and 38 us.
+//
+// |u| |E| bounds every product and running sum, and with it the logits' error
+// (logit_error in router_select.cuh).  Two warps sum the tokens' squares from each
+// stage in shared memory once its products are done (5 us of the 41); then it is
+// free.  The experts' are summed by the epilogue warps from global memory before
+// the first products are done.
 constexpr int BK = 64;                 // bf16 K elements per 128-byte swizzle row
 constexpr int TM = 128;                // token rows per CTA (TMEM lanes)
 constexpr int kMaxN = 256;
-constexpr int kChunk = 8;
-constexpr int KW = 2;                 // blocks of 64 columns per stage
-constexpr int STAGES = 6 / KW;
+constexpr int kChunk = 4;
+constexpr int STAGES = 6;              // of a block each
 constexpr int kEpiWarps = 16;          // four per TMEM lane quarter, 16-column pieces in turn
-constexpr int kTcThreads = 64 + 32 * kEpiWarps;
+constexpr int kSqWarps = 2;            // square sums
+constexpr int kTcThreads = 64 + 32 * (kEpiWarps + kSqWarps);
 constexpr int kPieces = kMaxN / 16 / (kEpiWarps / 4);
+constexpr int kMaxE2 = 1024 / kEpiWarps;   // blocks that sum experts' squares
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int A_BOX = TM * BK * 2, B_BOX = (kMaxN / 2) * BK * 2;
-constexpr int A_BYTES = KW * A_BOX, B_BYTES = KW * B_BOX;
-constexpr int OFF_B = STAGES * A_BYTES;
-constexpr int OFF_BAR = OFF_B + STAGES * B_BYTES;
-constexpr int N_BARS = 2 * STAGES + 5;           // full, empty, tfull[2], tempty[2], mma_done
+constexpr int OFF_B = STAGES * A_BOX;
+constexpr int OFF_BAR = OFF_B + STAGES * B_BOX;
+constexpr int N_BARS = 3 * STAGES + 5;   // full, used, empty, tfull[2], tempty[2], mma_done
 constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
-constexpr int SMEM_BYTES = OFF_MISC + 16;
+constexpr int OFF_EMAX = OFF_MISC + 16;          // an epilogue warp's largest square sum each
+constexpr int SMEM_BYTES = OFF_EMAX + kEpiWarps * 4;
+static_assert(OFF_BAR % 8 == 0, "barriers");
 constexpr int SMEM_ALLOC = SMEM_BYTES + 1024;
 
 // Partial logits of the tensor-core path: groups of 32 tokens, [ld / 8][32][8]
@@ -79,6 +89,11 @@ struct LogitParams {
   int n_tt, n_et, Nt;       // token tiles of 256, expert tiles of Nt
   int ld;                   // n_et * Nt
   float* P;                 // S slices of groups of 32 tokens (tc_row)
+  const __nv_bfloat16* E;
+  int d;
+  float* u2;                // square sums of the tokens' slices: [S][whole groups of 32 tokens]
+  float* e2;                // [n_e2]: the largest square sum of a block's experts
+  int n_e2;
   int32_t* counts;          // zeroed here, as is the listing's length
   int32_t* n_listed;        // two lengths
   int* err;
@@ -87,6 +102,22 @@ struct LogitParams {
 __device__ __forceinline__ void raise_abort(volatile int* abort, int* err) {
   *abort = 1;
   atomicOr(err, ERR_GEMM_TIMEOUT);
+}
+
+// Adds the squares of eight bf16 values to s and their bits to any.  Four squares
+// are added in bf16 (at most three roundings of 2^-8: s is a bound's scale).
+__device__ __forceinline__ void add_squares(const uint4& v, float& s, uint32_t& any) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+  __nv_bfloat162 a = __hmul2(h[0], h[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) a = __hfma2(h[i], h[i], a);
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&a);
+  s += __uint_as_float(w << 16) + __uint_as_float(w & 0xffff0000u);
+  any |= v.x | v.y | v.z | v.w;
+}
+// A square sum as a bound: 0 for zeros alone, and never 0 by underflow.
+__device__ __forceinline__ float square_bound(float s, uint32_t any) {
+  return (any & 0x7fff7fffu) == 0u ? 0.f : s < 1e-30f ? 1e-30f : s;
 }
 
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -98,19 +129,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint8_t* sA = smem;
   uint8_t* sB = smem + OFF_B;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
-  uint64_t* empty = full + STAGES;
+  uint64_t* used = full + STAGES;       // the stage's products are done
+  uint64_t* empty = used + STAGES;      // and its tokens have been squared
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* mma_done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  float* emax = reinterpret_cast<float*>(smem + OFF_EMAX);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t half = cluster_ctarank();           // which 128 tokens, which half of the experts
   const bool is_leader = half == 0;
   const int Nt = p.Nt;
 
   if (warp == 0 && lane == 0) {
-    for (int s = 0; s < STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&used[s], 1);
+      mbar_init(&empty[s], kSqWarps);
+    }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 2 * kEpiWarps);          // the epilogue warps of both CTAs
@@ -150,19 +187,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int et = it % p.n_et, sl = (it / p.n_et) % p.S, tt = it / p.n_et / p.S;
         const int row0 = tt * 2 * TM + (int)half * TM, e0 = et * Nt + (int)half * (Nt / 2);
         const int kb1 = (sl + 1) * p.nk / p.S;
-        for (int kb = sl * p.nk / p.S; kb < kb1; kb += KW) {
+        for (int kb = sl * p.nk / p.S; kb < kb1; ++kb) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitNs)) {
             raise_abort(abort_flag, p.err);
             ok = false;
             break;
           }
-          const int n = min(KW, kb1 - kb);
-          if (is_leader) mbar_arrive_expect_tx(&full[stage], (uint32_t)n * bytes);
+          if (is_leader) mbar_arrive_expect_tx(&full[stage], bytes);
           const uint32_t fb = full_leader0 + stage * 8;
-          for (int i = 0; i < n; ++i) {
-            tma_load_2d_pair(sA + stage * A_BYTES + i * A_BOX, &tmU, (kb + i) * BK, row0, fb);
-            tma_load_2d_pair(sB + stage * B_BYTES + i * B_BOX, &tmE, (kb + i) * BK, e0, fb);
-          }
+          tma_load_2d_pair(sA + stage * A_BOX, &tmU, kb * BK, row0, fb);
+          tma_load_2d_pair(sB + stage * B_BOX, &tmE, kb * BK, e0, fb);
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
       }
@@ -181,47 +215,98 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int it = first; it < items && ok; it += step) {
         const int sl = (it / p.n_et) % p.S;
         const int kb0 = sl * p.nk / p.S, kb1 = (sl + 1) * p.nk / p.S;
-        for (int c0 = kb0; c0 < kb1 && ok; c0 += kChunk) {
-          if (!mbar_wait_bounded(&tempty[buf], tphase ^ 1, abort_flag, kWaitNs)) {
+        for (int kb = kb0; kb < kb1; ++kb) {
+          const bool first_of = (kb - kb0) % kChunk == 0;
+          const bool last_of = (kb - kb0 + 1) % kChunk == 0 || kb + 1 == kb1;
+          if ((first_of && !mbar_wait_bounded(&tempty[buf], tphase ^ 1, abort_flag, kWaitNs)) ||
+              !mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitNs)) {
             raise_abort(abort_flag, p.err);
             ok = false;
             break;
           }
           tc_fence_after();
-          const int c1 = min(kb1, c0 + kChunk);
-          for (int kb = c0; kb < c1; kb += KW) {
-            if (!mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitNs)) {
-              raise_abort(abort_flag, p.err);
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const int n = min(KW, c1 - kb);
-            for (int i = 0; i < n; ++i) {
-              const uint32_t a0 = smem_u32(sA + stage * A_BYTES + i * A_BOX);
-              const uint32_t b0 = smem_u32(sB + stage * B_BYTES + i * B_BOX);
+          const uint32_t a0 = smem_u32(sA + stage * A_BOX), b0 = smem_u32(sB + stage * B_BOX);
 #pragma unroll
-              for (int k = 0; k < BK / 16; ++k)
-                mma2_f16_ss(tmem_base + buf * kMaxN, smem_desc_k_sw128(a0 + k * 32),
-                            smem_desc_k_sw128(b0 + k * 32), idesc,
-                            (kb > c0 || i > 0 || k > 0) ? 1u : 0u);
-            }
-            mma2_commit_mask(&empty[stage], 3);
-            if (++stage == STAGES) { stage = 0; phase ^= 1; }
+          for (int k = 0; k < BK / 16; ++k)
+            mma2_f16_ss(tmem_base + buf * kMaxN, smem_desc_k_sw128(a0 + k * 32),
+                        smem_desc_k_sw128(b0 + k * 32), idesc, (!first_of || k > 0) ? 1u : 0u);
+          mma2_commit_mask(&used[stage], 3);
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+          if (last_of) {
+            mma2_commit_mask(&tfull[buf], 3);
+            if (++buf == 2) { buf = 0; tphase ^= 1; }
           }
-          if (!ok) break;
-          mma2_commit_mask(&tfull[buf], 3);
-          if (++buf == 2) { buf = 0; tphase ^= 1; }
         }
       }
       mma2_commit_local(mma_done);
       mbar_wait_bounded(mma_done, 0, nullptr, kWaitNs);
     }
+  } else if (warp >= 2 + kEpiWarps) {
+    // ------------------------------------------------------------ square sums (both CTAs)
+    // A lane takes 16 bytes of every fourth of its warp's 64 token rows (a row is
+    // 128 bytes a block, in any order).
+    const int w = warp - 2 - kEpiWarps;
+    constexpr int kRows = TM / kSqWarps / 4;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int it = first; it < items && ok; it += step) {
+      const int et = it % p.n_et, sl = (it / p.n_et) % p.S, tt = it / p.n_et / p.S;
+      const int kb1 = (sl + 1) * p.nk / p.S;
+      float sq[kRows];
+      uint32_t any[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) { sq[r] = 0.f; any[r] = 0u; }
+      for (int kb = sl * p.nk / p.S; kb < kb1; ++kb) {
+        const bool got = mbar_wait_bounded(&used[stage], phase, abort_flag, kWaitNs);
+        if (!__all_sync(0xffffffffu, got)) {
+          if (lane == 0) raise_abort(abort_flag, p.err);
+          ok = false;
+          break;
+        }
+        if (et == 0) {
+          const uint4* rows =
+              reinterpret_cast<const uint4*>(sA + stage * A_BOX) + w * (kRows * 32) + lane;
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) add_squares(rows[r * 32], sq[r], any[r]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+      }
+      if (!ok) break;
+      if (et == 0) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) {              // the row's eight lanes
+            sq[r] += __shfl_xor_sync(0xffffffffu, sq[r], o);
+            any[r] |= __shfl_xor_sync(0xffffffffu, any[r], o);
+          }
+          const int row = tt * 2 * TM + (int)half * TM + (w * kRows + r) * 4 + (lane >> 3);
+          if ((lane & 7) == 0 && row < p.T)
+            p.u2[(size_t)sl * token_groups(p.T) * 32 + row] = square_bound(sq[r], any[r]);
+        }
+      }
+    }
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
-    const int q = warp & 3, part = (warp - 2) >> 2;
+    const int w = warp - 2, q = warp & 3, part = w >> 2;
     const int n_pieces = Nt / 16;
     const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    // the experts' square sums, a warp per expert
+    float e_top = 0.f;
+    for (int e = blockIdx.x * kEpiWarps + w; e < p.N_r; e += gridDim.x * kEpiWarps) {
+      const uint4* row = reinterpret_cast<const uint4*>(p.E + (size_t)e * p.d);
+      const int nv = p.d / 8;
+      float sq = 0.f;
+      uint32_t any = 0u;
+#pragma unroll 8
+      for (int v = lane; v < nv; v += 32) add_squares(__ldg(row + v), sq, any);
+      const float b = square_bound(sel_warp_sum(sq), __reduce_or_sync(0xffffffffu, any));
+      e_top = fmaxf(e_top, b == b ? b : 1e-30f);         // NaN: its logits are NaN either way
+    }
+    if (lane == 0) emax[w] = e_top;
     int buf = 0;
     uint32_t tphase = 0;
     bool ok = true;
@@ -275,6 +360,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && blockIdx.x < p.n_e2) {
+    float e_top = 0.f;
+    for (int w = 0; w < kEpiWarps; ++w) e_top = fmaxf(e_top, emax[w]);
+    p.e2[blockIdx.x] = e_top;
+  }
   cluster_sync_all();          // no CTA leaves while the other may still use its barriers or TMEM
   if (warp == 1) {
     tc_fence_after();
@@ -478,7 +568,8 @@ __global__ void __launch_bounds__(128) router_logits64_kernel(
 // The tokens listed for the exact pass: how many, their ids, and 32 words of
 // experts that the open decisions wait for (word l, bit j: expert j*32 + l);
 // and those of them whose every logit has to be exact: how many, ids, finished shares and
-// float64 logits [T][N_r].
+// float64 logits [T][N_r].  u2, e2: the square sums that router_logits_tc_kernel
+// left (LogitParams), n_e2 of the latter.
 struct Recheck {
   int32_t* n;             // [2]
   int32_t* tok;
@@ -486,36 +577,45 @@ struct Recheck {
   int32_t* full_tok;
   int32_t* full_done;
   double* full_x;
+  float* u2;
+  float* e2;
+  int n_e2;
 };
 
-// x[j]: the slices' sums, joined in slice order; returns the largest sum over
-// slices of |partial| among this lane's experts.
-template <int V>
-__device__ __forceinline__ float join_slices(const float* __restrict__ row, int S, size_t stride,
-                                             int N, float (&x)[V]) {
-  const int lane = threadIdx.x & 31;
-  float m[V], mag = 0.f;
+// The largest square sum of an expert, by a warp.
+__device__ __forceinline__ float largest_e2(const Recheck& rc) {
+  constexpr int kMost = (kMaxE2 + 31) / 32;
+  float v = 0.f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    x[j] = j * 32 + lane < N ? row[tc_col(j * 32 + lane)] : 0.f;
-    m[j] = fabsf(x[j]);
+  for (int i = 0; i < kMost; ++i) {
+    const int at = i * 32 + (threadIdx.x & 31);
+    v = fmaxf(v, at < rc.n_e2 ? rc.e2[at] : 0.f);
   }
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));   // no sign, no NaN
+}
+// Bound on the error of token t's logits, by a warp (S <= kMaxSlices < 32 slices).
+__device__ __forceinline__ float token_error(const Recheck& rc, int S, int T, int t, float e2) {
+  const int lane = threadIdx.x & 31;
+  const float v = lane < S ? rc.u2[(size_t)lane * token_groups(T) * 32 + t] : 0.f;
+  return logit_error(sel_warp_sum(v), e2);
+}
+
+// x[j]: the slices' sums, joined in slice order.
+template <int V>
+__device__ __forceinline__ void join_slices(const float* __restrict__ row, int S, size_t stride,
+                                            int N, float (&x)[V]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < V; ++j) x[j] = j * 32 + lane < N ? row[tc_col(j * 32 + lane)] : 0.f;
   for (int s = 1; s < S; ++s) {
     row += stride;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float v = j * 32 + lane < N ? row[tc_col(j * 32 + lane)] : 0.f;
-      x[j] += v;
-      m[j] += fabsf(v);
-    }
+    for (int j = 0; j < V; ++j) x[j] += j * 32 + lane < N ? row[tc_col(j * 32 + lane)] : 0.f;
   }
-#pragma unroll
-  for (int j = 0; j < V; ++j) mag = fmaxf(mag, m[j]);
-  return mag;
 }
 
 template <int V>
-__global__ void __launch_bounds__(128) router_select_kernel(
+__global__ void __launch_bounds__(128, V <= 8 ? 7 : 1) router_select_kernel(
     const float* __restrict__ P, int S, int ld, const float* __restrict__ bias, int T,
     SelectRule r, int32_t* __restrict__ idx, float* __restrict__ gate,
     int32_t* __restrict__ counts, float* __restrict__ logits, Recheck rc) {
@@ -527,19 +627,21 @@ __global__ void __launch_bounds__(128) router_select_kernel(
   __syncthreads();
   pdl_wait();
   pdl_trigger();
+  const float e2 = largest_e2(rc);
   for (int t = blockIdx.x * wpb + warp; t < T; t += gridDim.x * wpb) {
     float x[V], sc[V], key[V];
-    const float mag = sel_warp_max(join_slices<V>(P + tc_row(t, ld), S, slice_stride(T, ld), N, x));
+    const float logit_err = token_error(rc, S, T, t, e2);
+    const bool wide = logit_err > kWideError;            // every logit from float64
+    join_slices<V>(P + tc_row(t, ld), S, slice_stride(T, ld), N, x);
     if (logits) {
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if (j * 32 + lane < N) logits[(size_t)t * N + j * 32 + lane] = x[j];
     }
-    const float logit_err = mag == 0.f ? 0.f : kLogitError * fmaxf(4.f, mag);
     int32_t* ti = idx + (size_t)t * r.K;
     const TokenScale ts = select_keys<V>(x, bias, r, logit_err, sc, key);
-    const Selection sel = select_core<V>(key, ts.err, r, wk, ti);
-    if (sel.open) {
+    const Selection sel = select_core<V>(key, ts, bias, r, wk, ti);
+    if (sel.open || wide) {
       int slot = 0;
       if (lane == 0) {
         slot = atomicAdd(rc.n, 1);
@@ -549,7 +651,9 @@ __global__ void __launch_bounds__(128) router_select_kernel(
       uint32_t mask = sel.mask;
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        if (j * 32 + lane < N && takes_part(key[j], sel.lo, sel.hi, ts.err)) mask |= 1u << j;
+        if (j * 32 + lane < N &&
+            (wide || takes_part(key[j], key_error(ts.top, key[j]), sel.lo, sel.hi)))
+          mask |= 1u << j;
       rc.mask[(size_t)slot * 32 + lane] = mask;
       continue;                                     // its gates and load come with the exact pass
     }
@@ -568,7 +672,7 @@ __global__ void __launch_bounds__(128) router_select_kernel(
 //           float64 logits, kDots at a time, their products spread over the
 //           block (exact in float32 unless below 2^-126).  Usually two or
 //           three experts and one turn.
-// Latency-bound (at T 8192 some 50 tokens are listed), so a thread has two
+// Latency-bound (at T 8192 some 700 tokens are listed), so a thread has two
 // vectors of every row in flight at once (one where a block has more threads
 // than 256); four of them, or more registers than let three blocks share an
 // SM, cost more tokens what they save few: T 1024 55 us, T 256 26 against 36
@@ -584,16 +688,17 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) router_token_kernel
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ double part[MAXT / 32][kDots];
   __shared__ int n_want;
-  __shared__ uint32_t red[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = r.N_r, nv = d / 8;
   const BlockRoute b = block_route_smem(smem_raw, N, r.K);
   pdl_wait();
   pdl_trigger();
   const int n = all_tokens ? T : rc.n[0];
+  const float e2 = EXACT ? 0.f : largest_e2(rc);
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int t = all_tokens ? i : rc.tok[i];
     double a = 0.0;
-    float mag = 0.f;
+    const float logit_err = EXACT ? 0.f : token_error(rc, S, T, t, e2);
+    const bool wide = logit_err > kWideError;            // every logit from float64
     if (tid < N) {
       if (EXACT) {
         const size_t at = (size_t)t * ld + tid, stride = (size_t)T * ld;
@@ -602,24 +707,14 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) router_token_kernel
         // as the first pass joined them
         const size_t at = tc_row(t, ld) + tc_col(tid), stride = slice_stride(T, ld);
         float f = static_cast<const float*>(P)[at];
-        mag = fabsf(f);
-        for (int s = 1; s < S; ++s) {
-          const float v = static_cast<const float*>(P)[at + s * stride];
-          f += v;
-          mag += fabsf(v);
-        }
+        for (int s = 1; s < S; ++s) f += static_cast<const float*>(P)[at + s * stride];
         a = (double)f;
       }
       if (logits) logits[(size_t)t * N + tid] = (float)a;
     }
-    float logit_err = 0.f;
-    if (!EXACT) {
-      mag = __uint_as_float(block_max(__float_as_uint(mag), red));
-      logit_err = mag == 0.f ? 0.f : kLogitError * fmaxf(4.f, mag);
-    }
     if (tid < N) {
       b.x[tid] = a;
-      b.exact_f[tid] = EXACT || mag == 0.f;
+      b.exact_f[tid] = EXACT || logit_err == 0.f;
     }
     const auto fetch = [&](int nl) {
       if (EXACT) return;                            // nothing is wanted
@@ -673,11 +768,11 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) router_token_kernel
         __syncthreads();
       }
     };
-    if (!EXACT && !all_tokens && mag != 0.f) {
+    if (!EXACT && logit_err != 0.f && (wide || !all_tokens)) {
       // the experts that the first pass found wanting
       if (tid == 0) n_want = 0;
       __syncthreads();
-      const bool want = tid < N && ((rc.mask[(size_t)i * 32 + lane] >> warp) & 1u);
+      const bool want = tid < N && (wide || ((rc.mask[(size_t)i * 32 + lane] >> warp) & 1u));
       if (want) b.list[atomicAdd(&n_want, 1)] = (uint16_t)tid;
       __syncthreads();
       fetch(n_want);
@@ -797,9 +892,12 @@ size_t tc_ws_bytes(int T, int d, int N, Recheck* rc, uint8_t* base) {
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes, 256); return at; };
   take(slice_rows(T, L.n_et) * L.ld * 4);
+  const size_t u2 = take(slice_rows(T, L.n_et) * 4), e2 = take(kMaxE2 * 4);
   const size_t n = take(8), tok = take((size_t)T * 4), mask = take((size_t)T * 128), ftok = take((size_t)T * 4),
                fdone = take((size_t)T * 4), fx = take((size_t)T * N * 8);
   if (rc) {
+    rc->u2 = reinterpret_cast<float*>(base + u2);
+    rc->e2 = reinterpret_cast<float*>(base + e2);
     rc->n = reinterpret_cast<int32_t*>(base + n);
     rc->tok = reinterpret_cast<int32_t*>(base + tok);
     rc->mask = reinterpret_cast<uint32_t*>(base + mask);
@@ -811,7 +909,7 @@ size_t tc_ws_bytes(int T, int d, int N, Recheck* rc, uint8_t* base) {
 }
 
 moe_status launch_logits_tc(const void* u, const void* E, int T, int d, int N, float* P,
-                            int32_t* counts, int32_t* n_listed, cudaStream_t s) {
+                            int32_t* counts, Recheck* rc, cudaStream_t s) {
   const LogitTiling L = logit_tiling(T, d, N);
   CUtensorMap tmU, tmE;
   moe_status st = make_tmap_2d(&tmU, u, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d, T, BK, TM);
@@ -829,14 +927,21 @@ moe_status launch_logits_tc(const void* u, const void* E, int T, int d, int N, f
   p.ld = L.ld;
   p.P = P;
   p.counts = counts;
-  p.n_listed = n_listed;
+  p.n_listed = rc->n;
+  p.E = static_cast<const __nv_bfloat16*>(E);
+  p.d = d;
+  p.u2 = rc->u2;
+  p.e2 = rc->e2;
   p.err = device_error_word();
   if (!p.err) return fail(MOE_ERR_CUDA, "device error word unavailable");
-  const int pairs = resident_pairs();
+  const int resident = resident_pairs(), pairs = resident < kPairs ? resident : kPairs;
   if (pairs <= 0) return fail(MOE_ERR_CUDA, "router_logits: no resident CTA pair");
   const long long items = (long long)L.n_tt * L.n_et * L.S;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (unsigned)(items < pairs ? items : pairs));
+  // every block of the grid, or as many as have an expert
+  const int with_experts = (N + kEpiWarps - 1) / kEpiWarps;
+  p.n_e2 = rc->n_e2 = with_experts < (int)cfg.gridDim.x ? with_experts : (int)cfg.gridDim.x;
   cfg.blockDim = dim3(kTcThreads);
   cfg.dynamicSmemBytes = SMEM_ALLOC;
   cfg.stream = s;
@@ -906,10 +1011,10 @@ moe_status launch_route_scored(const void* u, const void* E, moe_dtype dt, const
   moe_status st;
   if (dt == MOE_BF16 && T > kFewTokens) {
     float* P = static_cast<float*>(ws);
-    Recheck rc;
+    Recheck rc{};
     tc_ws_bytes(T, d, N_r, &rc, static_cast<uint8_t*>(ws));
     const LogitTiling L = logit_tiling(T, d, N_r);
-    st = launch_logits_tc(u, E, T, d, N_r, P, counts, rc.n, s);
+    st = launch_logits_tc(u, E, T, d, N_r, P, counts, &rc, s);
     if (st != MOE_OK) return st;
     // a sigmoid needs no other logit: only softmax tokens can ask for all of them
     const bool full = score == MOE_SCORE_SOFTMAX;
@@ -933,7 +1038,7 @@ moe_status launch_route_scored(const void* u, const void* E, moe_dtype dt, const
 #undef MOE_SELECT
     if (st != MOE_OK) return st;
     st = launch_router_token<false>(u, E, P, L.S, L.ld, b, T, d, r, idx, gate, counts, nullptr, rc,
-                                    false, 2 * sm_count(), s);
+                                    false, 3 * sm_count(), s);
     return st == MOE_OK && full ? launch_router_full(u, E, b, d, r, idx, gate, counts, rc, s) : st;
   }
   double* P = static_cast<double*>(ws);

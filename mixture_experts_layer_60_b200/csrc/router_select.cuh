@@ -69,21 +69,56 @@ struct SelectRule {
   float scale;
 };
 
-// Bound on a float32 logit's error per unit of max(4, largest |logit|).  The
-// tensor-core sums are cut every 32 accumulation steps; over N(0,1) rows at
-// d = 512 to 16384 their largest error was 3.1e-6 with logits up to 5.2, where
-// this bound is 1.3e-5.
-constexpr float kLogitError = 2.5e-6f;
+// Bound on a tensor-core logit's error, from the square sums of the token's and
+// of the largest expert's values.  A step of 16 products cuts each of them at
+// 2^-25 and its sum at 2^-23 of the step's largest product or running sum A (a
+// model, fitted to large values held over chains of small ones): at most 6e-7 A.
+// A chunk sums 16 steps from zero, and a sum that is large and then cancels has
+// A <= |u| |E| / 2 over the chunk's columns, which summed over the chunks is at
+// most |u| |E| / 2 of the whole rows: 4.8e-6 |u| |E|, and the chunks' sums round
+// as they join.  Rows made for it were measured to reach 2.8e-6 (cuts of half on
+// average), N(0,1) rows 6e-8.  (A bound that follows the logits instead lists
+// fewer of those and is wrong where large products cancel.)
+constexpr float kLogitError = 5e-6f;
+// Past this the scores' error is no longer their slope's: every logit is made exact.
+constexpr float kWideError = 0.25f;
+__device__ __forceinline__ float logit_error(float u2, float e2) {
+  if (u2 == 0.f || (e2 == 0.f && u2 < INFINITY)) return 0.f;   // zeros: exact
+  if (u2 != u2) return 1e-30f;                                 // every logit is NaN, exactly
+  const float e = kLogitError * sqrtf(u2) * sqrtf(e2);
+  return e <= kWideError ? fmaxf(e, 1e-30f) : INFINITY;
+}
 
-// Per token: the softmax's largest logit and sum, and the error bound of its
-// float32 keys: |key error| <= err + kKeyRounding |key|.
+// Per token: the softmax's largest logit and sum, and the bound on a float32
+// key's error against the others', from its score s:
+//   slope s (1 - s)   sigmoid; softmax with a bias (twice: its sum's error too)
+//   slope s           softmax without: the sum's error scales every score alike
+// plus `flat` for the float32 functions and kKeyRounding |key|.  top: the largest
+// (0: exact).
 struct TokenScale {
-  float m, z, err;
+  float m, z, slope, flat, top;
+  bool whole;                    // slope s
+  __device__ __forceinline__ float score_error(float s) const {
+    return fmaf(slope, whole ? s : s * (1.f - s), flat);
+  }
 };
 constexpr float kKeyRounding = 1.2e-7f;
+__device__ __forceinline__ TokenScale exact_scale() {
+  return TokenScale{0.f, 1.f, 0.f, 0.f, 0.f, true};
+}
+// The slope for logits off by at most dx <= kWideError, over which a score's own
+// slope grows by at most e^(4 dx) <= 1 + 8 dx.
+__device__ __forceinline__ float error_slope(float dx, bool softmax, bool bias) {
+  return dx * fmaf(8.f, dx, 1.f) * (softmax && bias ? 2.f : 1.f);
+}
+// A key's whole error (an infinite key has none).
+__device__ __forceinline__ float key_error(float score_error, float key) {
+  return fabsf(key) < INFINITY ? fmaf(kKeyRounding, fabsf(key), score_error) : 0.f;
+}
 
 // Float32 keys and scores of a row of float32 logits.  logit_err: bound on
-// their error.  d s = s(1-s) dx (sigmoid), at most 2 s(1-s) max|dx| (softmax);
+// their error (past kWideError: of no use, the caller has every logit made
+// exact).  d s = s(1-s) dx (sigmoid), at most 2 s(1-s) max|dx| (softmax);
 // the fast exponential and division cost a score of size s at most 8 * 2^-23 s
 // (the exponential's argument error, |x| 2^-23, is weighted by s(1-s) or by
 // s ln(smax / s) < 0.4 smax).
@@ -92,7 +127,7 @@ __device__ __forceinline__ TokenScale select_keys(const float (&x)[V], const flo
                                                   const SelectRule& r, float logit_err,
                                                   float (&sc)[V], float (&key)[V]) {
   const int lane = threadIdx.x & 31, N = r.N_r;
-  TokenScale ts{0.f, 1.f, 0.f};
+  TokenScale ts = exact_scale();
   const bool softmax = r.score == MOE_SCORE_SOFTMAX;
   if (logit_err == 0.f) {
     // a row of exact zeros (a padding token): every score is 1/2, or 1/N_r
@@ -129,31 +164,39 @@ __device__ __forceinline__ TokenScale select_keys(const float (&x)[V], const flo
       sc[j] = j * 32 + lane < N ? __fdividef(x[j] < 0.f ? e : 1.f, 1.f + e) : 0.f;
     }
   }
+  ts.whole = softmax && !bias;
   float w = 0.f, s = 0.f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int e = j * 32 + lane;
     key[j] = e < N ? (bias ? sc[j] + bias[e] : sc[j]) : -INFINITY;
-    w = fmaxf(w, sc[j] * (1.f - sc[j]));
+    w = fmaxf(w, ts.whole ? sc[j] : sc[j] * (1.f - sc[j]));
     s = fmaxf(s, sc[j]);
   }
   // non-negative floats compare as integers
   w = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(w)));
   s = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s)));
-  ts.err = logit_err * w * (softmax ? 2.f : 1.f) + 9.6e-7f * s;
+  ts.slope = error_slope(fminf(logit_err, kWideError), softmax, bias != nullptr);
+  ts.flat = 9.6e-7f * s;
+  ts.top = fmaf(ts.slope, w, ts.flat);
   return ts;
 }
 
 // What a warp's selection decided: lane k's expert of slot k (k < 32; every
-// slot is in idx), whether a decision is open, the keys between which the
-// open decisions of the order lie (none: lo > hi), and this lane's experts
-// (bit j) that an open choice of groups waits for.
+// slot is in idx), whether a decision is open, the range of keys that the open
+// decisions of the order lie in (none: lo > hi), and this lane's experts (bit j)
+// that an open choice of groups waits for.
 struct Selection {
   int e;
   bool open;
   float lo, hi;
   uint32_t mask;
 };
+
+// Whether an expert with this key can take part in the open decisions.
+__device__ __forceinline__ bool takes_part(float key, float err, float lo, float hi) {
+  return key + err >= lo && key - err <= hi;
+}
 
 // The sizes at which a group's keys and their sum are rounded (a sum may be far
 // smaller than its keys); 0 where one is infinite: no rounding moves that score.
@@ -162,20 +205,14 @@ __device__ __forceinline__ float group_rounding(float a, float b) {
   return v < INFINITY ? v : 0.f;
 }
 
-// Whether an expert with this key can take part in the open decisions.
-__device__ __forceinline__ bool takes_part(float key, float lo, float hi, float err) {
-  const float pad = 3.f * err + 2.f * kKeyRounding * fabsf(key);
-  return key >= lo - pad && key <= hi + pad;
-}
-
-// key: this lane's keys, off by at most err + kKeyRounding |key| (err == 0:
-// exact).  wk: N_r floats of shared memory for this warp.
+// key: this lane's keys, off by what ts says.  wk: N_r floats of shared memory for
+// this warp.
 template <int V>
-__device__ __forceinline__ Selection select_core(const float (&key)[V], float err,
-                                                 const SelectRule& r, float* wk,
+__device__ __forceinline__ Selection select_core(const float (&key)[V], const TokenScale& ts,
+                                                 const float* bias, const SelectRule& r, float* wk,
                                                  int32_t* __restrict__ idx) {
   const int lane = threadIdx.x & 31, N = r.N_r;
-  const float rel = err > 0.f ? kKeyRounding : 0.f;
+  const float err = ts.top, rel = err > 0.f ? kKeyRounding : 0.f;
   Selection out{0, false, INFINITY, -INFINITY, 0u};
   uint32_t ko[V];
 #pragma unroll
@@ -270,7 +307,9 @@ __device__ __forceinline__ Selection select_core(const float (&key)[V], float er
   }
   // K rounds of a warp arg-max, and one more for the best expert left out;
   // lane k % 32 keeps and writes winner k
-  float prev = INFINITY;
+  float prev = INFINITY, won = 0.f;
+  int n = 0;
+  const bool few = r.K < 32;                         // a lane for every round
   for (int k = 0; k <= r.K; ++k) {
     uint32_t lb = ko[0];
     int lj = 0;
@@ -281,21 +320,55 @@ __device__ __forceinline__ Selection select_core(const float (&key)[V], float er
     if (mx == 0u) break;                             // nothing eligible is left
     const int be = __reduce_min_sync(0xffffffffu, lb == mx ? lj * 32 + lane : 0x7fffffff);
     const float v = sel_val(mx);
-    if (prev - v < 2.f * err + rel * (fabsf(prev) + fabsf(v))) {
-      out.open = true;
-      out.lo = fminf(out.lo, v);
-      out.hi = fmaxf(out.hi, prev);
+    if (!few) {                                      // by the largest error of all
+      const float ev = key_error(err, v), ep = key_error(err, prev);
+      if (err > 0.f && prev - v < ev + ep) {
+        out.lo = fminf(out.lo, v - ev);
+        out.hi = fmaxf(out.hi, prev + ep);
+      }
+      prev = v;
     }
-    prev = v;
+    if (lane == (k & 31)) {
+      won = v;
+      if (few || k < r.K) out.e = be;
+      if (k < r.K) idx[k] = be;
+    }
+    n = k + 1;
     if (k == r.K) break;
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (j * 32 + lane == be) ko[j] = 0u;
-    if (lane == (k & 31)) {
-      out.e = be;
-      idx[k] = be;
+  }
+  if (few && err > 0.f) {
+    // lane k: winner k against the one before, each by its own error
+    float ke = 0.f;
+    if (lane < n) {
+      const float be = bias ? bias[out.e] : 0.f;
+      // a score regained from its key is off by the key's rounding
+      ke = key_error(fabsf(be) <= 4.f ? ts.score_error(won - be) + 5e-7f * ts.slope : err, won);
+    }
+    const float lo = won - ke, hi = won + ke;
+    const float up_lo = __shfl_up_sync(0xffffffffu, lo, 1), up_hi = __shfl_up_sync(0xffffffffu, hi, 1);
+    if (lane > 0 && lane < n && hi > up_lo) {
+      out.lo = lo;
+      out.hi = up_hi;
+    }
+    // the last one kept against every expert left out: none has a larger key than
+    // the best of them, nor an error past the largest
+    float rest = __shfl_sync(0xffffffffu, won + key_error(err, won), r.K & 31);
+    if (n <= r.K) rest = -INFINITY;
+    const float last_lo = __shfl_sync(0xffffffffu, lo, r.K - 1);
+    const float last_hi = __shfl_sync(0xffffffffu, hi, r.K - 1);
+    if (rest > last_lo) {
+      out.lo = fminf(out.lo, last_lo);
+      out.hi = fmaxf(out.hi, last_hi);
+    }
+    if (__any_sync(0xffffffffu, out.lo <= out.hi)) {
+      out.lo = -sel_warp_max(-out.lo);
+      out.hi = sel_warp_max(out.hi);
     }
   }
+  out.open = out.open || out.lo <= out.hi;
   return out;
 }
 
@@ -361,6 +434,7 @@ struct BlockRoute {
   uint32_t* ord;      // [N] keys in order form
   uint32_t* best;     // [warps][block_keep(K)] each warp's best eligible keys in order (0: none)
   float* top_key;     // [K + 1] keys in order, the best one left out last
+  float* top_err;     // [K + 1] their errors
   uint16_t* top_id;   // [K + 1] their experts
   uint16_t* list;     // [N] experts whose exact logit is wanted
   uint8_t* exact_f;   // [N]
@@ -375,7 +449,7 @@ __host__ __device__ __forceinline__ int block_best(int N, int K) {
 }
 __host__ __device__ inline size_t block_route_bytes(int N, int K) {
   return (size_t)N * 8 + 8 + ((size_t)N + 4) * 4 + (size_t)block_best(N, K) * 4 +
-         ((size_t)K + 2) * 8 + (size_t)N * 2 + N + 16;
+         ((size_t)K + 2) * 12 + (size_t)N * 2 + N + 16;
 }
 __device__ __forceinline__ BlockRoute block_route_smem(uint8_t* p, int N, int K) {
   BlockRoute b;
@@ -383,7 +457,8 @@ __device__ __forceinline__ BlockRoute block_route_smem(uint8_t* p, int N, int K)
   b.ord = reinterpret_cast<uint32_t*>(p + (size_t)((N + 1) / 2 * 2) * 8);   // 16-byte aligned
   b.best = b.ord + (N + 3) / 4 * 4;                                         // 16-byte aligned
   b.top_key = reinterpret_cast<float*>(b.best + block_best(N, K));
-  b.top_id = reinterpret_cast<uint16_t*>(b.top_key + K + 1);
+  b.top_err = b.top_key + K + 1;
+  b.top_id = reinterpret_cast<uint16_t*>(b.top_err + K + 1);
   b.list = b.top_id + K + 1;
   b.exact_f = reinterpret_cast<uint8_t*>(b.list + N);
   return b;
@@ -423,7 +498,8 @@ __device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRul
   __shared__ uint32_t red_m[32], red_w[32], red_s[32];
   __shared__ float gkey[32][2];
   __shared__ unsigned s_near;
-  __shared__ int n_list, s_lo, s_hi;
+  __shared__ int n_list;
+  __shared__ uint32_t s_lo, s_hi;      // the keys, in order form, between which open pairs lie
   const int e = threadIdx.x, N = r.N_r, K = r.K, lane = e & 31;
   const bool softmax = r.score == MOE_SCORE_SOFTMAX, mine = e < N;
   const bool grouped = r.topk_groups < r.n_groups, two = r.group_top == 2;
@@ -447,19 +523,26 @@ __device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRul
       s = ex ? (float)sel_sigmoid(x) : sel_sigmoid((float)x);
     }
     const float key = bias ? s + bi : s;
-    // error of the inexact keys, and of the softmax's sum, which exact keys share
-    float err = 0.f, eta = 0.f, smax = 0.f;
+    // errors of the keys, and of the softmax's sum, which exact ones share
+    TokenScale ts = exact_scale();
+    float eta = 0.f, smax = 0.f, ke = 0.f;
     if (!all) {
+      ts.whole = softmax && !bias;
       // non-negative floats compare as whole numbers (fmaxf drops a NaN)
-      const float w = __uint_as_float(block_max(__float_as_uint(fmaxf(0.f, s * (1.f - s))), red_w));
+      const float w = __uint_as_float(
+          block_max(__float_as_uint(fmaxf(0.f, ts.whole ? s : s * (1.f - s))), red_w));
       smax = __uint_as_float(block_max(__float_as_uint(fmaxf(0.f, s)), red_s));
-      err = logit_err * w * (softmax ? 2.f : 1.f) + 4.8e-7f * smax;
+      ts.slope = error_slope(logit_err, softmax, bias != nullptr);
+      ts.flat = 4.8e-7f * smax;
+      ts.top = fmaf(ts.slope, w, ts.flat);
       eta = softmax ? logit_err : 0.f;
+      if (mine && !ex) ke = key_error(ts.score_error(s), key);
+      if (mine && ex && softmax) ke = key_error(bias ? 2.f * eta * s : 0.f, key);
     }
-    const float rel = err > 0.f ? kKeyRounding : 0.f;
+    const float err = ts.top, rel = err > 0.f ? kKeyRounding : 0.f;
     uint32_t o = mine ? sel_ord(key) : 0u;
     if (mine) b.ord[e] = o;
-    if (e == 0) { n_list = 0; s_lo = 0x7fffffff; s_hi = -1; s_near = 0u; }
+    if (e == 0) { n_list = 0; s_lo = 0xffffffffu; s_hi = 0u; s_near = 0u; }
     if (e < 32) gkey[e][0] = gkey[e][1] = 0.f;
     __syncthreads();
     bool want = false, z_open = false;
@@ -551,27 +634,32 @@ __device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRul
     const bool placed = mine && o != 0u && place <= K;
     if (placed) {
       b.top_key[place] = key;
+      b.top_err[place] = ke;
       b.top_id[place] = (uint16_t)e;
     }
     const int n_top = __syncthreads_count(placed);   // K + 1, or K where no other is eligible
     bool open = false;
     if (!all) {
-      for (int k = e; k + 1 < n_top; k += blockDim.x) {
-        const float a = b.top_key[k], c = b.top_key[k + 1];
-        if (b.exact_f[b.top_id[k]] && b.exact_f[b.top_id[k + 1]]) {
-          // only the softmax's sum is left to tell them apart
-          const float sa = bias ? a - bias[b.top_id[k]] : a, sb = bias ? c - bias[b.top_id[k + 1]] : c;
-          if (eta > 0.f && a - c <= eta * fabsf(sa - sb) + 2.f * kKeyRounding * fmaxf(fabsf(a), fabsf(c)))
+      // key a of expert ia comes before key c of expert ic: may their errors turn
+      // them around?  Of two exact keys only the softmax's sum's can.
+      const auto pair = [&](float a, float ea, int ia, float c, float ec, int ic) {
+        if (b.exact_f[ia] && b.exact_f[ic]) {
+          const float gap = bias ? fabsf((a - bias[ia]) - (c - bias[ic])) : 0.f;
+          if (eta > 0.f && a - c <= 2.f * eta * gap + 2.f * kKeyRounding * fmaxf(fabsf(a), fabsf(c)))
             z_open = true;
-        } else if (a - c < 2.f * err + rel * (fabsf(a) + fabsf(c))) {
-          atomicMin(&s_lo, k + 1);                   // places between which the open pairs lie
-          atomicMax(&s_hi, k + 1);
+        } else if (a - c < ea + ec) {
+          atomicMin(&s_lo, sel_ord(c - ec));
+          atomicMax(&s_hi, sel_ord(a + ea));
         }
-      }
+      };
+      for (int k = e; k + 1 < n_top; k += blockDim.x)
+        pair(b.top_key[k], b.top_err[k], b.top_id[k], b.top_key[k + 1], b.top_err[k + 1],
+             b.top_id[k + 1]);
+      // the last one kept against the experts further down
+      if (o != 0u && !placed) pair(b.top_key[K - 1], b.top_err[K - 1], b.top_id[K - 1], key, ke, e);
       if (__syncthreads_or(z_open)) return false;
-      if (s_hi >= 0 && mine && !ex) {
-        want = want || takes_part(key, b.top_key[s_hi], b.top_key[s_lo - 1], err);
-      }
+      if (s_hi != 0u && o != 0u && !ex)
+        want = want || takes_part(key, ke, sel_val(s_lo), sel_val(s_hi));
       open = __syncthreads_or(want);
     }
     if (!open) break;

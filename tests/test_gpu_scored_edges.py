@@ -143,6 +143,85 @@ def test_equal_gate_gradients_leave_the_balance_term_alone(score, T, N, K):
     assert (np.abs(f64(dl) - want) <= 2.0 ** -20 * 2 * f64(coef).max()).all()
 
 
+# ------------------------------------------------------------------ sums that cancel
+
+def _cancelling(kind, T, d, N, seed):
+    u, E, b = _normal(T, d, N, seed)
+    if kind.startswith("pair"):
+        _, a, c0, c1 = kind.split("_")
+        c0, c1 = int(c0), int(c1) % d
+        u[:, c0], u[:, c1] = float(a), -float(a)
+        E[:, c0] = E[:, c1] = 1.0
+    elif kind == "mean":
+        u = (u.float() + 30).to(BF)
+        E = (E.float() - E.float().mean(1, keepdim=True)).to(BF)
+    elif kind == "outliers":
+        k = torch.randperm(d // 2, generator=_gen(seed), device="cuda")[:6]
+        u[:, k] = 1000.0
+        u[:, k + d // 2] = -1000.0
+        E[:, k + d // 2] = E[:, k]
+    elif kind == "coherent":
+        # running sums rise over half of every 512 columns and come back
+        g = _gen(seed + 1)
+        u = (4 + 0.4 * torch.randn(T, d, generator=g, device="cuda")).to(BF)
+        sign = 1 - 2.0 * (torch.arange(d, device="cuda") // 256 % 2)
+        mag = 1 + 0.1 * torch.randn(N, d, generator=g, device="cuda")
+        E = (sign * mag * d ** -0.5).to(BF)
+    elif kind == "vanish":
+        # every float32 logit is 0, the exact ones are not: the small term meets a large sum
+        e = E[:, 2].clone()
+        u[:], E[:] = 0, 0
+        u[:, 0], u[:, 20], u[:, 40] = 256.0, 2.0 ** -18, -256.0
+        E[:, 0] = E[:, 40] = 1.0
+        E[:, 20] = (e.float() * d ** 0.5).to(BF)
+        b = None
+    return u, E, b
+
+
+KINDS = ["pair_64_3_4", "pair_64_0_511", "pair_256_5_-3", "pair_4096_0_1", "pair_4096_16_200",
+         "mean", "outliers", "coherent", "vanish"]
+
+
+@pytest.mark.parametrize("T", [300, 1500])
+@pytest.mark.parametrize("d,N,K", [(512, 64, 6), (7168, 256, 8), (2048, 96, 8)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_selection_of_cancelling_rows(kind, d, N, K, T):
+    u, E, b = _cancelling(kind, T, d, N, 17)
+    _check_selection(u, E, b, K, SIG)
+    _check_selection(u, E, b, K, SOFT, n_groups=8, topk_groups=4, group_top=2, renorm=False)
+
+
+@pytest.mark.parametrize("T", [40, 1500])
+def test_selection_of_rows_of_zeros_among_others(T):
+    """Padding tokens tie everywhere; other rows whose logits are 0 in float32 do not."""
+    u, E, _ = _cancelling("vanish", T, 512, 64, 3)
+    u[::3] = 0
+    u[1::3] = -0.0
+    for score in (SIG, SOFT):
+        _check_selection(u, E, None, 6, score)
+
+
+@pytest.mark.parametrize("T", [300, 1500])
+@pytest.mark.parametrize("score", [SIG, SOFT])
+def test_selection_of_rows_of_nan(T, score):
+    """Every key of a token with a NaN is NaN, and NaN keys are equal: the lowest ids, in the
+    lowest groups."""
+    u, E, b = _normal(T, 256, 64, 19)
+    clean = _route(u, E, b, 6, score=score)[0]
+    rows = [0, 7, T - 1]
+    bad = u.clone()
+    bad[rows[0]] = float("nan")
+    bad[rows[1], 9] = float("nan")
+    bad[rows[2], 200] = float("nan")
+    for kw in (dict(), dict(n_groups=8, topk_groups=4, group_top=2)):
+        idx = _route(bad, E, b, 6, score=score, **kw)[0]
+        for r in rows:
+            assert idx[r].tolist() == list(range(6)), idx[r]
+        if not kw:
+            keep = [t for t in range(T) if t not in rows]
+            assert torch.equal(idx[keep], clean[keep])
+
+
 # ------------------------------------------------------------------ groups
 
 @pytest.mark.parametrize("T", [64, 1300])
@@ -200,27 +279,29 @@ def test_groups_of_large_biases_that_cancel(T):
     logit's error.  Where the float32 logit puts a key on the other side of a rounding than the
     exact one, two groups that tie do not seem to."""
     N, G, d = 64, 32, 7168
-    u, E, _ = _normal(T, d, N, 800)
-    lg = torch.empty(T, N, device="cuda")
-    _route(u, E, None, 8, logits=lg)
-    x = f64(u) @ f64(E).T
     base = np.where(np.arange(N) % 2 == 0, 8000.0, -8000.0).astype(np.float32)
-    exact, seen = S.keys(x, base, S.SIGMOID), S.keys(f64(lg), base, S.SIGMOID)
-    found = np.argwhere(exact != seen)
-    assert len(found) >= 3
-    for t, e in found[:12]:
-        a = e // 2
-        up = seen[t, e] > exact[t, e]
-        if a == (0 if up else G - 1):
-            continue
-        c = (a - 1 if up else a + 1)               # ties keep the lower group
-        others = [g for g in range(G) if g not in (a, c)]
-        b = base.copy()
-        for k, g in enumerate(others):
-            b[2 * g] += 100 if k < 15 else -100    # surely kept, surely not
-        score = exact[t].reshape(G, 2).sum(1)
-        b[2 * c] += score[a] - score[c]            # a whole number of steps: now they tie
-        bt = torch.from_numpy(b).cuda()
-        idx, _, _ = _route(u, E, bt, 16, n_groups=G, topk_groups=16, group_top=2)
-        want = S.select(S.keys(x[t:t + 1], b, S.SIGMOID), 16, G, 16, 2)[0]
-        assert np.array_equal(idx[t].cpu().numpy(), want), (t, e, a, c)
+    seen_any = 0
+    for seed in range(800, 804):
+        u, E, _ = _normal(T, d, N, seed)
+        lg = torch.empty(T, N, device="cuda")
+        _route(u, E, None, 8, logits=lg)
+        x = f64(u) @ f64(E).T
+        exact, seen = S.keys(x, base, S.SIGMOID), S.keys(f64(lg), base, S.SIGMOID)
+        for t, e in np.argwhere(exact != seen)[:6]:
+            a = e // 2
+            up = seen[t, e] > exact[t, e]
+            if a == (0 if up else G - 1):
+                continue
+            seen_any += 1
+            c = (a - 1 if up else a + 1)               # ties keep the lower group
+            others = [g for g in range(G) if g not in (a, c)]
+            b = base.copy()
+            for k, g in enumerate(others):
+                b[2 * g] += 100 if k < 15 else -100    # surely kept, surely not
+            score = exact[t].reshape(G, 2).sum(1)
+            b[2 * c] += score[a] - score[c]            # a whole number of steps: now they tie
+            bt = torch.from_numpy(b).cuda()
+            idx, _, _ = _route(u, E, bt, 16, n_groups=G, topk_groups=16, group_top=2)
+            want = S.select(S.keys(x[t:t + 1], b, S.SIGMOID), 16, G, 16, 2)[0]
+            assert np.array_equal(idx[t].cpu().numpy(), want), (t, e, a, c)
+    assert seen_any
