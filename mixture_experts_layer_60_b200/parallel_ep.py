@@ -26,7 +26,7 @@ import torch
 
 from . import (moe_combine, moe_ep_dispatch, moe_ep_plan, moe_ep_return, moe_expert_ffn,
                moe_expert_ffn_workspace_size, moe_permute_index, moe_permute_workspace_size,
-               moe_route, moe_route_scored, moe_route_scored_workspace_size,
+               moe_route, moe_route_grouped, moe_route_scored, moe_route_scored_workspace_size,
                moe_route_workspace_size, MOE_BF16, MOE_F32, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX)
 from .configs import LayerConfig
 
@@ -105,6 +105,8 @@ class _EPRank:
                              n_groups=c.n_groups, topk_groups=c.topk_groups,
                              group_top=c.group_top, renorm=c.renorm, gate_scale=c.gate_scale,
                              stream=stream)
+        elif c.n_groups > 1:
+            moe_route_grouped(u, self.E, self.b, c.K, c.n_groups, c.topk_groups, *out, stream)
         else:
             moe_route(u, self.E, self.b, c.K, *out, stream)
         # the grouping only: moe_ep_dispatch copies the rows from u itself

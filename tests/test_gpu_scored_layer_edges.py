@@ -1,0 +1,37 @@
+"""MoELayer and expert-parallel ranks with the scored router's choices: one rounding of du, streams,
+memory kept by 8-bit checkpoints, the selection that the balance loss counts, FP8 and float32."""
+from dataclasses import replace
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_60_b200 as moe
+from mixture_experts_layer_60_b200.configs import LayerConfig
+from mixture_experts_layer_60_b200.layer import MoELayer
+from mixture_experts_layer_60_b200.parallel_ep import EPGroupEmulated
+from mixture_experts_layer_60_b200.synth import make_layer_inputs, step_u, upstream_grad
+from oracle import moe_scored as S
+from tests.harness import TOL, assert_close, f64
+
+pytestmark = pytest.mark.gpu
+
+BASE = LayerConfig("scored", T=150, d=256, N_r=16, K=3, N_s=1, I=256, dtype="bf16", seed=43,
+                   bias="uniform")
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(group_top=2, gate_scale=2.0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_expert_parallel_ranks_keep_the_group_limit(kw, dtype):
+    cfg = replace(BASE, n_groups=4, topk_groups=2, dtype=dtype, **kw)
+    w = make_layer_inputs(cfg, "cuda")
+    us = [step_u(cfg, s, "cuda") for s in range(2)]
+    us[1] = us[1][:33].contiguous()
+    ep = EPGroupEmulated(cfg, w, 2, T_max=cfg.T)
+    hs = [h.clone() for h in ep.forward(us)]
+    torch.cuda.synchronize()
+    for s, u in enumerate(us):
+        one = MoELayer(cfg, w, T_max=u.shape[0])
+        want = one.forward(u)
+        assert torch.equal(ep.ranks[s].topk_idx[:u.shape[0]], one.topk_idx)
+        assert torch.equal(hs[s], want)
