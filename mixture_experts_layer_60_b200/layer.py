@@ -17,6 +17,8 @@ module only allocates buffers and sequences calls.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import (MOE_BF16, MOE_E4M3, MOE_F32, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX,
@@ -39,6 +41,15 @@ GAMMA = 0.001
 
 def _ws(nbytes, device):
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+
+
+def _on(stream):
+    """The stream of a step as PyTorch's current one: what a step's buffers are cleared or
+    filled with comes before the step's kernels."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream")
+                             else torch.cuda.ExternalStream(int(stream)))
 
 
 class MoELayer:
@@ -132,7 +143,8 @@ class MoELayer:
         c = self.cfg
         T = u.shape[0]
         if T != self.T_alloc:
-            self._alloc(T)
+            with _on(stream):
+                self._alloc(T)
         st = torch.cuda.current_stream() if stream is None else stream
         pe = phase_events or {}
         if gate_up_events:
@@ -254,9 +266,11 @@ class MoELayer:
             raise ValueError("the backward is implemented for bf16 and FP8 layers")
         T = u.shape[0]
         if T != self.T_alloc:
-            self._alloc(T)
+            with _on(stream):
+                self._alloc(T)
         if getattr(self, "T_train", None) != T:
-            self._alloc_train(T)
+            with _on(stream):
+                self._alloc_train(T)
         self._route(u, stream, getattr(self, "logits", None))
         (wgu, sgu), (wdn, sdn) = self.W["W_gate_up"], self.W["W_down"]
         (wsgu, ssgu), (wsdn, ssdn) = self.W["Ws_gate_up"], self.W["Ws_down"]

@@ -35,3 +35,40 @@ def test_expert_parallel_ranks_keep_the_group_limit(kw, dtype):
         want = one.forward(u)
         assert torch.equal(ep.ranks[s].topk_idx[:u.shape[0]], one.topk_idx)
         assert torch.equal(hs[s], want)
+
+
+def test_first_training_step_on_a_stream_of_its_own():
+    """Buffers that a first step makes are ready on the step's stream, whatever the current one
+    is busy with."""
+    cfg = replace(BASE, score="softmax")
+    w = make_layer_inputs(cfg, "cuda")
+    dh = upstream_grad(cfg, "cuda")
+    ref = MoELayer(cfg, w)
+    ref.forward_train(w["u"])
+    want = ref.backward(dh).clone()
+    lay = MoELayer(cfg, w)
+    st = torch.cuda.Stream()
+    junk = [torch.full((cfg.T, cfg.K), float("nan"), device="cuda") for _ in range(16)]
+    torch.cuda.synchronize()
+    del junk                                       # their memory is handed out next
+    torch.cuda._sleep(int(3e8))                    # the current stream is busy for a while
+    lay.forward_train(w["u"], stream=st)
+    got = lay.backward(dh, stream=st)
+    st.synchronize()
+    got = got.cpu()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want.cpu())
+
+
+def test_a_new_token_count_on_a_stream_of_its_own():
+    """Nothing that the layer clears for a new token count is cleared after the step has used it."""
+    cfg = replace(BASE, score="softmax")
+    w = make_layer_inputs(cfg, "cuda")
+    lay = MoELayer(cfg, w)
+    u = w["u"][:70].contiguous()
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(int(3e8))
+    lay.forward(u, stream=st)
+    torch.cuda.synchronize()
+    assert int(lay.counts.sum()) == int(lay.offsets[-1]) == 70 * cfg.K
