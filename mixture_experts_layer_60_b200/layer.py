@@ -227,7 +227,8 @@ class MoELayer:
         self.d_logit = torch.empty(T, c.K, dtype=torch.float32, device=dev)
         self.d_logit_perm = torch.empty(R, dtype=torch.float32, device=dev)
         self.dx_perm = torch.empty(R, c.d, dtype=bf, device=dev)
-        self.dx_s = torch.empty(c.N_s, T, c.d, dtype=bf, device=dev)
+        # a scored router's own part of du lies behind the shared experts'
+        self.dx_s = torch.empty(c.N_s + c.scored, T, c.d, dtype=bf, device=dev)
         self.du = torch.empty(T, c.d, dtype=bf, device=dev)
         dt = MOE_E4M3 if self.fp8 else MOE_BF16
         size = moe_expert_ffn_backward8_workspace_size if c.checkpoint8 \
@@ -360,18 +361,16 @@ class MoELayer:
                                g["Ws_gate_up"][j:j + 1], g["Ws_down"][j:j + 1], stream, None,
                                sl(ssgu, j), sl(ssdn, j))
         if c.scored:
-            # residual, shared and routed gradients (the combine with weights
-            # 1), then the router's own added in place
-            moe_combine(dh, self.dx_s if c.N_s else None, self.dx_perm, self.inv_row, self.ones,
-                        self.du, stream)
+            # the router's own gradient, then residual, shared, routed and router
+            # gradients in one sum (the combine with weights 1), rounded once
             bal = c.balance_alpha > 0
-            moe_route_scored_backward(u, self.E, self.logits, self.topk_idx, self.d_gate, self.du,
-                                      g["E"], self.route_bwd_ws, score=self.score,
-                                      renorm=c.renorm, gate_scale=c.gate_scale,
+            moe_route_scored_backward(u, self.E, self.logits, self.topk_idx, self.d_gate,
+                                      self.dx_s[c.N_s], g["E"], self.route_bwd_ws,
+                                      score=self.score, renorm=c.renorm, gate_scale=c.gate_scale,
                                       seq_offsets=self.seq_offsets if bal else None,
                                       balance_coef=self.balance_coef if bal else None,
-                                      d_loss=d_balance if bal else None, du_base=self.du,
-                                      stream=stream)
+                                      d_loss=d_balance if bal else None, stream=stream)
+            moe_combine(dh, self.dx_s, self.dx_perm, self.inv_row, self.ones, self.du, stream)
             return self.du
         moe_unpermute_backward(dh, self.dx_s if c.N_s else None, self.dx_perm, self.inv_row,
                                self.topk_idx, self.d_logit, self.E, self.du, stream)

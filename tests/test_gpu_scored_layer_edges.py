@@ -72,3 +72,32 @@ def test_a_new_token_count_on_a_stream_of_its_own():
     lay.forward(u, stream=st)
     torch.cuda.synchronize()
     assert int(lay.counts.sum()) == int(lay.offsets[-1]) == 70 * cfg.K
+
+
+@pytest.mark.parametrize("kw", [dict(score="softmax"), dict(renorm=False, N_s=0),
+                                dict(balance_alpha=0.05, N_s=2)])
+def test_du_of_a_scored_layer_is_rounded_once(kw):
+    """du is the sum of dh, the experts' and the router's parts, each of them bf16 (half a step,
+    2^-8 of the value, lies in the router's), rounded once (2^-8) from float32 sums (2^-18)."""
+    cfg = replace(BASE, **kw)
+    w = make_layer_inputs(cfg, "cuda")
+    lay = MoELayer(cfg, w)
+    lay.forward_train(w["u"])
+    dh = upstream_grad(cfg, "cuda")
+    du = lay.backward(dh)
+    T, N, d = cfg.T, cfg.N_r, cfg.d
+    dl = torch.empty(T, N, device="cuda")
+    bal = cfg.balance_alpha > 0
+    moe.moe_route_scored_backward(w["u"], w["E"], lay.logits, lay.topk_idx, lay.d_gate,
+                                  torch.empty_like(w["u"]), torch.empty(N, d, device="cuda"),
+                                  lay.route_bwd_ws, score=lay.score, renorm=cfg.renorm,
+                                  gate_scale=cfg.gate_scale,
+                                  balance_coef=lay.balance_coef if bal else None, d_logit=dl)
+    router = f64(dl) @ f64(w["E"])
+    parts = [f64(dh), router] + [f64(lay.dx_s[j]) for j in range(cfg.N_s)] + \
+        [f64(lay.dx_perm)[lay.inv_row.cpu().numpy()[:, k]] for k in range(cfg.K)]
+    want, mag = sum(parts), sum(np.abs(p) for p in parts)
+    tol = 2.0 ** -8 * (np.abs(want) + np.abs(router)) + 2.0 ** -15 * np.abs(f64(dl)) @ np.abs(f64(w["E"])) \
+        + 2.0 ** -18 * mag
+    err = np.abs(f64(du) - want)
+    assert (err <= tol).all(), f"{(err > tol).sum()} of {err.size}, worst {(err / tol).max():.2f}"
