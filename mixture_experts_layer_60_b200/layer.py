@@ -118,6 +118,8 @@ class MoELayer:
             self.u_s = torch.empty(T, d // 128, dtype=torch.float32, device=dev)
             self.x_scale = torch.empty(R, d // 128, dtype=torch.float32, device=dev)
         self.T_alloc = T
+        if c.checkpoint8:
+            self.T_train = None                # h lies in a training step's workspace
 
     def _route(self, u, stream, logits=None):
         c = self.cfg
@@ -211,15 +213,27 @@ class MoELayer:
         c, dev = self.cfg, self.device
         R, bf = T * c.K, torch.bfloat16
         hdt = torch.uint8 if self.fp8 else bf
+        dt = MOE_E4M3 if self.fp8 else MOE_BF16
         if c.checkpoint8:
             # pre-activations as E4M3 codes and a scale for each row and 128 columns
             pair = lambda rows: (torch.empty(rows, 2 * c.I, dtype=torch.uint8, device=dev),
                                  torch.empty(rows, 2 * c.I // 128, dtype=torch.float32, device=dev))
             self.a_gu, self.a_s = pair(R), [pair(T) for _ in range(c.N_s)]
+            # the forward's h is not kept: it lies where the backward forms h again,
+            # the last R rows of its workspace, the shared experts' behind it
+            size = moe_expert_ffn_backward8_workspace_size
+            at = size(dt, R, c.d, c.I, c.N_r) - 2 * R * c.I
+            rows = R + c.N_s * T
+            self.h_all = self.h_mid = None
+            self.bwd_ws = _ws(max(at + 2 * rows * c.I, size(dt, T, c.d, c.I, 1)), dev)
+            self.h_all = self.bwd_ws[at:at + 2 * rows * c.I].view(bf).view(rows, c.I)
+            self.h_mid, self.h_s = self.h_all[:R], self.h_all[R:].view(c.N_s, T, c.I)
         else:
             self.a_gu = torch.empty(R, 2 * c.I, dtype=bf, device=dev)
             self.a_s = torch.empty(c.N_s, T, 2 * c.I, dtype=bf, device=dev)
-        self.h_s = torch.empty(c.N_s, T, c.I, dtype=hdt, device=dev)
+            self.h_s = torch.empty(c.N_s, T, c.I, dtype=hdt, device=dev)
+            size = moe_expert_ffn_backward_workspace_size
+            self.bwd_ws = _ws(max(size(dt, R, c.d, c.I, c.N_r), size(dt, T, c.d, c.I, 1)), dev)
         self.h_s_scale = torch.empty(c.N_s, T, c.I // 128, dtype=torch.float32, device=dev) \
             if self.fp8 else None
         self.dy_perm = torch.empty(R, c.d, dtype=bf, device=dev)
@@ -230,10 +244,6 @@ class MoELayer:
         # a scored router's own part of du lies behind the shared experts'
         self.dx_s = torch.empty(c.N_s + c.scored, T, c.d, dtype=bf, device=dev)
         self.du = torch.empty(T, c.d, dtype=bf, device=dev)
-        dt = MOE_E4M3 if self.fp8 else MOE_BF16
-        size = moe_expert_ffn_backward8_workspace_size if c.checkpoint8 \
-            else moe_expert_ffn_backward_workspace_size
-        self.bwd_ws = _ws(max(size(dt, R, c.d, c.I, c.N_r), size(dt, T, c.d, c.I, 1)), dev)
         if c.scored:
             rdt = MOE_F32 if self.E.dtype == torch.float32 else MOE_BF16
             self.logits = torch.empty(T, c.N_r, dtype=torch.float32, device=dev)

@@ -101,3 +101,44 @@ def test_du_of_a_scored_layer_is_rounded_once(kw):
         + 2.0 ** -18 * mag
     err = np.abs(f64(du) - want)
     assert (err <= tol).all(), f"{(err > tol).sum()} of {err.size}, worst {(err / tol).max():.2f}"
+
+
+@pytest.mark.parametrize("N_s", [0, 1, 2])
+def test_checkpoint8_keeps_fewer_bytes(N_s):
+    """What a layer holds after a training step: 2.06 I bytes of codes and scales a row instead
+    of 4 I of pre-activations; the forward's h lies where the backward forms it again."""
+    cfg = replace(BASE, T=2048, K=4, N_s=N_s, d=256, I=512)
+    w = make_layer_inputs(cfg, "cuda")
+    dh = upstream_grad(cfg, "cuda")
+    held = {}
+    for c8 in (False, True):
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        lay = MoELayer(replace(cfg, checkpoint8=c8), w)
+        lay.forward_train(w["u"])
+        lay.backward(dh)
+        torch.cuda.synchronize()
+        held[c8] = torch.cuda.memory_allocated() - before
+        del lay
+    rows, I = cfg.T * (cfg.K + N_s), cfg.I
+    want = rows * (4 * I - 2 * I - 2 * I / 32)     # bytes that the codes and scales free
+    # buffers are handed out in blocks of 512 bytes and up to 2 MB
+    assert held[False] - held[True] >= 0.9 * want, (held, want)
+
+
+def test_checkpoint8_layer_changes_its_token_count():
+    cfg = replace(BASE, checkpoint8=True, N_s=2)
+    w = make_layer_inputs(cfg, "cuda")
+    dh = upstream_grad(cfg, "cuda")
+    lay = MoELayer(cfg, w)
+    plain = MoELayer(replace(cfg, checkpoint8=False), w)
+    for T in (150, 70, 150):
+        u, g = w["u"][:T].contiguous(), dh[:T].contiguous()
+        assert torch.equal(lay.forward(u), plain.forward(u))
+        h = lay.forward_train(u).clone()
+        assert torch.equal(h, plain.forward_train(u))
+        first = lay.backward(g).clone()
+        # inference in between with another token count, then the step again
+        lay.forward(w["u"][:33].contiguous())
+        assert torch.equal(lay.forward_train(u), h)
+        assert torch.equal(lay.backward(g), first)
