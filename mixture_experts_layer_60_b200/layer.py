@@ -64,6 +64,9 @@ class MoELayer:
             raise ValueError(f"unknown router score {cfg.score!r}")
         if cfg.checkpoint8 and cfg.dtype != "bf16":
             raise ValueError("8-bit activation checkpoints are implemented for bf16 layers")
+        if cfg.checkpoint8 and (cfg.d % 256 or cfg.I % 256):
+            raise ValueError(f"8-bit activation checkpoints need d={cfg.d} and I={cfg.I} to be "
+                             "multiples of 256")
         self.score = MOE_SCORE_SOFTMAX if cfg.score == "softmax" else MOE_SCORE_SIGMOID
         if self.fp8:
             self.W = {k: self._quantise(weights[k]) for k in

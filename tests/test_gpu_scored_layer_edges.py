@@ -142,3 +142,11 @@ def test_checkpoint8_layer_changes_its_token_count():
         lay.forward(w["u"][:33].contiguous())
         assert torch.equal(lay.forward_train(u), h)
         assert torch.equal(lay.backward(g), first)
+
+
+@pytest.mark.parametrize("kw", [dict(d=384), dict(I=384)])
+def test_checkpoint8_refuses_its_shape_when_the_layer_is_made(kw):
+    cfg = replace(BASE, checkpoint8=True, **kw)
+    w = make_layer_inputs(cfg, "cuda")
+    with pytest.raises(ValueError, match="256"):
+        MoELayer(cfg, w)
