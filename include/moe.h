@@ -173,13 +173,15 @@ moe_status moe_route_scored(const void* u, const void* E, moe_dtype dt, const fl
  * moe_balance_loss - the sequence-wise balance loss (the pages name it with
  * its weight alpha; this is its usual formula).  With s' = s / sum_j s_j and
  * a sequence of n tokens,
- *   f_i = N_r / (K n) * number of its (token, slot) pairs routed to i
+ *   f_i = N_r / (K n) * number of its (token, slot) pairs with topk_idx = i
  *   P_i = 1/n * sum of its tokens' s'_i
  *   loss = alpha * sum_i f_i P_i
  *   coef_i = alpha * f_i / n = dloss / ds'_{t,i}  (the selection held fixed)
  *   logits      [T, N_r]      device, float32, from moe_route_scored
  *   topk_idx    [T, K]        device, int32 (an id outside [0, N_r) counts for
- *                             no expert)
+ *                             no expert): the routed choice, or, as DeepSeek-V3
+ *                             defines f_i, the top K of the scores themselves
+ *                             (moe_route_scored without bias and groups)
  *   seq_offsets [n_seq+1]     device, int32, non-decreasing: sequence q is
  *                             tokens [seq_offsets[q], seq_offsets[q+1]); NULL:
  *                             one sequence of all T (n_seq == 1).  Tokens

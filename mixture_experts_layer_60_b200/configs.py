@@ -33,6 +33,10 @@ class LayerConfig:
     renorm: bool = True      # gates divided by the sum of the selected scores
     gate_scale: float = 1.0  # gates multiplied by this
     balance_alpha: float = 0.0   # > 0: sequence-wise balance loss in training steps
+    # which choice its f_i count: the routed one (biased, group-limited), or the top K of
+    # the scores themselves over all experts, as DeepSeek-V3 defines the loss (a bias that
+    # evens out the routed load takes the loss's gradient with it, this one's not)
+    balance_unbiased: bool = False
     checkpoint8: bool = False    # bf16 training: activations kept in 8 bits (E4M3)
 
     @property

@@ -251,6 +251,10 @@ class MoELayer:
             rdt = MOE_F32 if self.E.dtype == torch.float32 else MOE_BF16
             self.logits = torch.empty(T, c.N_r, dtype=torch.float32, device=dev)
             self.ones = torch.ones(T, c.K, dtype=torch.float32, device=dev)
+            if c.balance_unbiased:
+                self.free_choice = (torch.empty(T, c.K, dtype=torch.int32, device=dev),
+                                    torch.empty(T, c.K, dtype=torch.float32, device=dev),
+                                    torch.empty(c.N_r, dtype=torch.int32, device=dev))
             self.route_bwd_ws = _ws(moe_route_scored_backward_workspace_size(rdt, T, c.d, c.N_r),
                                     dev)
         if not hasattr(self, "grad"):
@@ -274,7 +278,8 @@ class MoELayer:
         balance_alpha > 0, self.balance holds the balance loss of every
         sequence [seq_offsets[q], seq_offsets[q+1]) of the tokens (int32 on the
         device; default: one sequence of all of them); without a balance loss
-        they are not looked at."""
+        they are not looked at.  The loss counts the routed choice, or that of
+        the unbiased scores (balance_unbiased)."""
         c = self.cfg
         if c.dtype not in ("bf16", "e4m3"):
             raise ValueError("the backward is implemented for bf16 and FP8 layers")
@@ -312,19 +317,25 @@ class MoELayer:
         moe_combine(u, self.y_shared if c.N_s else None, self.y_perm, self.inv_row,
                     self.topk_gate, self.h_out, stream)
         if c.balance_alpha > 0:
-            self._balance(seq_offsets, stream)
+            self._balance(u, seq_offsets, stream)
         self._u = u
         return self.h_out
 
-    def _balance(self, seq_offsets, stream):
+    def _balance(self, u, seq_offsets, stream):
         c, T = self.cfg, self.T_train
+        idx = self.topk_idx
+        if c.balance_unbiased:
+            # the top K of the scores alone; gates and load of that choice are not used
+            idx, gate, counts = self.free_choice
+            moe_route_scored(u, self.E, None, c.K, idx, gate, counts, self.route_ws,
+                             score=self.score, stream=stream)
         n = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
         if getattr(self, "_balance_for", None) != (T, n):
             self.balance = torch.empty(n, dtype=torch.float32, device=self.device)
             self.balance_coef = torch.empty(n, c.N_r, dtype=torch.float32, device=self.device)
             self.balance_ws = _ws(moe_balance_loss_workspace_size(T, c.N_r, n), self.device)
             self._balance_for = (T, n)
-        moe_balance_loss(self.logits, self.topk_idx, c.balance_alpha, self.balance,
+        moe_balance_loss(self.logits, idx, c.balance_alpha, self.balance,
                          self.balance_coef, self.balance_ws, score=self.score,
                          seq_offsets=seq_offsets, stream=stream)
         self.seq_offsets = seq_offsets

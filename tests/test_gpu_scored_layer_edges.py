@@ -150,3 +150,38 @@ def test_checkpoint8_refuses_its_shape_when_the_layer_is_made(kw):
     w = make_layer_inputs(cfg, "cuda")
     with pytest.raises(ValueError, match="256"):
         MoELayer(cfg, w)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(score="softmax", renorm=False),
+                                dict(n_groups=4, topk_groups=2, group_top=2)])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_balance_loss_of_the_unbiased_choice(kw, dtype):
+    """f_i counts the top K of the scores over all experts, whatever bias and groups route."""
+    cfg = replace(BASE, balance_alpha=1.0, balance_unbiased=True, dtype=dtype, **kw)
+    w = make_layer_inputs(cfg, "cuda")
+    w["b"] = torch.linspace(0.4, -0.4, cfg.N_r, device="cuda")
+    off = [0, 40, 40, 130]
+    ot = torch.tensor(off, dtype=torch.int32, device="cuda")
+    lay = MoELayer(cfg, w)
+    routed = MoELayer(replace(cfg, balance_unbiased=False), w)
+    h = lay.forward_train(w["u"], seq_offsets=ot).clone()
+    assert torch.equal(h, routed.forward_train(w["u"], seq_offsets=ot)), "the loss routes nothing"
+    assert torch.equal(lay.topk_idx, routed.topk_idx) and torch.equal(lay.counts, routed.counts)
+    soft = cfg.score == "softmax"
+    x = f64(w["u"]) @ f64(w["E"]).T
+    idx = S.select(S.keys(x, None, S.SOFTMAX if soft else S.SIGMOID), cfg.K)
+    want, coef = S.balance(x, idx, off, 1.0, S.SOFTMAX if soft else S.SIGMOID)
+    # a score moves by at most its logit's error (5e-6 |u| |E|, some 1e-4 here)
+    assert_close(f64(lay.balance), want, 2e-4, "balance loss")
+    assert (np.abs(f64(lay.balance_coef) - coef) <= 2.0 ** -23 * coef).all()
+    assert not torch.equal(lay.balance, routed.balance)
+    # its gradient, without any of the gates'
+    dh = torch.zeros_like(w["u"])
+    lay.backward(dh)
+    t = torch.from_numpy(x).requires_grad_()
+    s = torch.softmax(t, 1) if soft else torch.sigmoid(t)
+    sn = s / s.sum(1, keepdim=True)
+    loss = sum((torch.from_numpy(coef[q]) * sn[a:b].sum(0)).sum()
+               for q, (a, b) in enumerate(zip(off[:-1], off[1:])))
+    loss.backward()
+    assert_close(f64(lay.grad["E"]), t.grad.numpy().T @ f64(w["u"]), 2e-3, "dE")
