@@ -576,10 +576,12 @@ moe_status moe_route_scored_backward(const void* u, const void* E, moe_dtype dt,
  * a_gu (bf16) and h, 6 I bytes a row, the backward keeps 2 I bytes and the
  * scales.  With a = x W_gate_up[g]^T (float32), per row and 128 columns,
  *   a_scale = amax/448 (1 if all zero),  a_q = E4M3_rne_satfinite(a / a_scale)
- * (IEEE float32 division), and the backward works from a' = a_q * a_scale:
+ * (IEEE float32 division; a NaN in the tile makes its scale and codes NaN), and
+ * the backward works from a' = a_q * a_scale:
  *   h' = SiLU(a'_gate) * a'_up (bf16; for dW_down)
  *   dA = [dh * a'_up * SiLU'(a'_gate) | dh * SiLU(a'_gate)],  dh = dy W_down[g]
- *   dx, dW_down = sum dy^T h', dW_gate_up as moe_expert_ffn_backward.
+ *   dx, dW_down = sum dy^T h', dW_gate_up as moe_expert_ffn_backward (dA rounded
+ * to bf16 for its two products).
  * MOE_BF16 only.  h [rows, I] is moe_expert_gate_up's, bit for bit, for the
  * down projection; it need not be kept for the backward.
  *   a_q [rows, 2I] device e4m3 (gate columns first), 16-byte aligned;

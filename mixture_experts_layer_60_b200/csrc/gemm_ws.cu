@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* mma_done = tempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
-  float* amax_x = reinterpret_cast<float*>(smem + OFF_AMAX);
+  uint32_t* amax_x = reinterpret_cast<uint32_t*>(smem + OFF_AMAX);
   uint64_t* xbar = reinterpret_cast<uint64_t*>(smem + OFF_XBAR);
   int* s_tmax = reinterpret_cast<int*>(smem + OFF_TMAX);
   long long* costs = reinterpret_cast<long long*>(smem + OFF_AMAX);   // before the first tile
@@ -624,15 +624,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (EPI == WS_SWIGLU_SAVE8) {
           // lane j of this warp: the largest |gate| and |up| of token c*32 + j
           // over this warp's 32 columns, then over the tile's 128
-          float mg = 0.f, mu = 0.f;
+          // (as whole numbers, in which a NaN is the largest: its tile is NaN)
+          uint32_t mg = 0u, mu = 0u;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const uint32_t a = __reduce_max_sync(0xffffffffu, r0[j] & 0x7fffffffu);
             const uint32_t b = __reduce_max_sync(0xffffffffu, r1[j] & 0x7fffffffu);
-            if (lane == j) { mg = __uint_as_float(a); mu = __uint_as_float(b); }
+            if (lane == j) { mg = a; mu = b; }
           }
           const int sl = ch * 2 + (int)(xit & 1u);
-          float* slot = amax_x + sl * 4 * 64;
+          uint32_t* slot = amax_x + sl * 4 * 64;
           slot[q * 64 + lane] = mg;
           slot[q * 64 + 32 + lane] = mu;
           __syncwarp();
@@ -646,10 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++xit;
 #pragma unroll
           for (int o = 0; o < 4; ++o) {
-            mg = fmaxf(mg, slot[o * 64 + lane]);
-            mu = fmaxf(mu, slot[o * 64 + 32 + lane]);
+            mg = max(mg, slot[o * 64 + lane]);
+            mu = max(mu, slot[o * 64 + 32 + lane]);
           }
-          const float sg = amax_scale(mg), su = amax_scale(mu);
+          const float sg = amax_scale(__uint_as_float(mg)), su = amax_scale(__uint_as_float(mu));
           // token c*32 + lane: its two scales, their reciprocals and a power of
           // two that brings values and scale into div_by's range (the quotient
           // is the same; an infinite scale divides finite values to 0), for
