@@ -185,3 +185,85 @@ def test_balance_loss_of_the_unbiased_choice(kw, dtype):
                for q, (a, b) in enumerate(zip(off[:-1], off[1:])))
     loss.backward()
     assert_close(f64(lay.grad["E"]), t.grad.numpy().T @ f64(w["u"]), 2e-3, "dE")
+
+
+VARIANTS = [dict(score="softmax"), dict(renorm=False, gate_scale=4.0, balance_alpha=0.02),
+            dict(gate_scale=2.5, n_groups=4, topk_groups=2, group_top=2, N_s=0)]
+
+
+@pytest.mark.parametrize("kw", VARIANTS)
+@pytest.mark.parametrize("dtype", ["f32", "e4m3"])
+def test_forward_of_other_types_with_the_scored_router(kw, dtype):
+    """Selection by the definition; h' from the layer's own expert outputs, gates and load:
+    float32 sums, rounded once."""
+    cfg = replace(BASE, dtype=dtype, **kw)
+    w = make_layer_inputs(cfg, "cuda")
+    lay = MoELayer(cfg, w)
+    h = lay.forward(w["u"])
+    x = f64(w["u"]) @ f64(w["E"]).T
+    score = S.SOFTMAX if cfg.score == "softmax" else S.SIGMOID
+    want = S.select(S.keys(x, w["b"].cpu().numpy(), score), cfg.K, cfg.n_groups, cfg.topk_groups,
+                    cfg.group_top)
+    assert np.array_equal(lay.topk_idx.cpu().numpy(), want)
+    assert np.array_equal(lay.counts.cpu().numpy(), np.bincount(want.reshape(-1), minlength=cfg.N_r))
+    g = S.gates(x, want, score, cfg.renorm, cfg.gate_scale)
+    # float32 layers route from float64 logits; bf16 inputs: 5e-6 |u| |E| of a logit, some 1e-4
+    assert_close(f64(lay.topk_gate), g, 1e-6 if dtype == "f32" else 4e-4, "gates")
+    rows = lay.inv_row.cpu().numpy()
+    parts = [f64(w["u"])] + [f64(lay.y_shared[j]) for j in range(cfg.N_s)] + \
+        [f64(lay.topk_gate)[:, k:k + 1] * f64(lay.y_perm)[rows[:, k]] for k in range(cfg.K)]
+    mag = sum(np.abs(p) for p in parts)
+    half = 2.0 ** -24 if dtype == "f32" else 2.0 ** -8
+    assert (np.abs(f64(h) - sum(parts)) <= half * np.abs(sum(parts)) + 2.0 ** -20 * mag).all()
+
+
+@pytest.mark.parametrize("kw", VARIANTS)
+def test_training_step_of_an_fp8_layer_with_the_scored_router(kw):
+    """The step's parts against each other: d_gate from the expert outputs, dE and the router's
+    share of du from d_gate by the definition, du their sum."""
+    cfg = replace(BASE, dtype="e4m3", **kw)
+    w = make_layer_inputs(cfg, "cuda")
+    lay = MoELayer(cfg, w)
+    h = lay.forward_train(w["u"]).clone()
+    assert torch.equal(h, MoELayer(cfg, w).forward(w["u"]))
+    dh = upstream_grad(cfg, "cuda")
+    du = lay.backward(dh)
+    torch.cuda.synchronize()
+    assert moe.moe_device_status() == 0
+    rows, idx = lay.inv_row.cpu().numpy(), lay.topk_idx.cpu().numpy()
+    y, g = f64(lay.y_perm), f64(dh)
+    dots = np.stack([(y[rows[:, k]] * g).sum(1) for k in range(cfg.K)], 1)
+    size = np.stack([np.abs(y[rows[:, k]] * g).sum(1) for k in range(cfg.K)], 1)
+    assert (np.abs(f64(lay.d_gate) - dots) <= 2.0 ** -18 * size).all()
+    score = S.SOFTMAX if cfg.score == "softmax" else S.SIGMOID
+    bal = cfg.balance_alpha > 0
+    x, T = f64(lay.logits), cfg.T
+    dl = S.backward(x, idx, f64(lay.d_gate), [0, T], f64(lay.balance_coef) if bal else None, None,
+                    score, cfg.renorm, cfg.gate_scale)
+    E, u = f64(w["E"]), f64(w["u"])
+    size = 2 * cfg.gate_scale * np.abs(f64(lay.d_gate)).sum(1, keepdims=True) + \
+        (2 * f64(lay.balance_coef).max() if bal else 0)          # of d_logit, 2^-20 of it its error
+    want = dl.T @ u
+    err = np.abs(f64(lay.grad["E"]) - want)
+    assert (err <= 2.0 ** -18 * (np.abs(dl).T @ np.abs(u)) + 2.0 ** -20 * (size * np.ones_like(dl)).T
+            @ np.abs(u)).all()
+    router = dl @ E
+    parts = [g, router] + [f64(lay.dx_s[j]) for j in range(cfg.N_s)] + \
+        [f64(lay.dx_perm)[rows[:, k]] for k in range(cfg.K)]
+    mag = sum(np.abs(p) for p in parts)
+    tol = 2.0 ** -8 * (np.abs(sum(parts)) + np.abs(router)) + 2.0 ** -18 * mag + \
+        2.0 ** -15 * (np.abs(dl) + size) @ np.abs(E)
+    assert (np.abs(f64(du) - sum(parts)) <= tol).all()
+    for k in ("W_gate_up", "W_down"):
+        assert torch.isfinite(lay.grad[k].float()).all()
+
+
+@pytest.mark.parametrize("kw", VARIANTS)
+def test_expert_parallel_float32_ranks_with_the_scored_router(kw):
+    cfg = replace(BASE, dtype="f32", **kw)
+    w = make_layer_inputs(cfg, "cuda")
+    us = [step_u(cfg, s, "cuda") for s in range(2)]
+    us[1] = us[1][:7].contiguous()
+    hs = [h.clone() for h in EPGroupEmulated(cfg, w, 2, T_max=cfg.T).forward(us)]
+    for s, u in enumerate(us):
+        assert torch.equal(hs[s], MoELayer(cfg, w, T_max=u.shape[0]).forward(u))
