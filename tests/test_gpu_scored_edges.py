@@ -222,6 +222,40 @@ def test_selection_of_rows_of_nan(T, score):
             assert torch.equal(idx[keep], clean[keep])
 
 
+@pytest.mark.parametrize("T", [40, 1300])
+@pytest.mark.parametrize("score", [SIG, SOFT])
+def test_selection_of_rows_past_every_bound(T, score):
+    """|u| |E| so large that the float32 logits say nothing: every logit is made exact."""
+    u, E, b = _cancelling("pair_65536_3_300", T, 512, 64, 41)
+    clean, _, _ = _normal(T, 512, 64, 41)
+    u[1::3] = clean[1::3]
+    _check_selection(u, E, b, 6, score)
+    _check_selection(u, E, b, 6, score, n_groups=8, topk_groups=4, group_top=2, renorm=False)
+
+
+@pytest.mark.parametrize("T", [9, 300, 1300])
+@pytest.mark.parametrize("score", [SIG, SOFT])
+def test_special_rows_route_as_few_tokens_do(T, score):
+    """Infinities of one or both signs, a NaN, huge and tiny rows: what the float64 path of a
+    few tokens says, beside ordinary rows."""
+    d, N, K = 256, 48, 5
+    u, E, b = _normal(T, d, N, 43)
+    u[1, 3] = float("inf")
+    u[2, 3], u[2, 9] = float("inf"), -float("inf")
+    u[3, 200] = float("nan")
+    u[4] *= 1e18
+    u[5] *= 1e-30
+    u[6, :] = -float("inf")
+    for kw in (dict(), dict(n_groups=6, topk_groups=3, group_top=2, renorm=False)):
+        idx, gate, _ = _route(u, E, b, K, score=score, **kw)
+        want, g, _ = _route(u[:8].contiguous(), E, b, K, score=score, **kw)
+        assert torch.equal(idx[:8], want), (idx[:8], want)
+        nan = torch.isnan(g)
+        assert torch.equal(torch.isnan(gate[:8]), nan)
+        # ordinary rows' gates come from float32 logits: 2 * 5e-6 |u| |E| of a gate
+        assert ((gate[:8] - g).abs()[~nan] <= 4e-4 * g.abs()[~nan] + 1e-30).all()
+
+
 # ------------------------------------------------------------------ groups
 
 @pytest.mark.parametrize("T", [64, 1300])
