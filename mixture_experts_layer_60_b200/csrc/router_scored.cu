@@ -966,12 +966,17 @@ size_t route_scored_ws_bytes(int T, int d, int N_r) {
   return a > b ? a : b;
 }
 
-// Tokens up to which the block path routes every token: a block per token
-// keeps a lone token's latency low, a warp per token costs a third of the
-// instructions.  d 7168, 256 experts, softmax and grouped sigmoid: T 256 23 us
-// by blocks and 29 by warps, T 1024 36 and 42 against 38 and 42, and warps win
-// beyond.
-constexpr int kBlockTokens = 1024;
+// Whether blocks route every token: a block per token keeps a lone token's latency
+// low, a warp per token costs a third of the instructions, and a block holds as
+// many threads as there are experts.  Blocks and warps, grouped sigmoid, us:
+//   d 7168, 256 experts: T 256 33 and 44, T 1024 51 and 53, T 2048 73 and 57
+//   d 2048,  64 experts: T 256 23 and 29, T 1024 31 and 30, T 2048 39 and 35
+//   d 4096, 1024 experts: T 64 46 and 72, T 256 68 and 77, T 512 103 and 72
+constexpr int kBlockTokens = 1024, kBlockExperts = 256;
+bool blocks_route(int T, int N_r) {
+  return (long long)T * (N_r > kBlockExperts ? N_r : kBlockExperts) <=
+         (long long)kBlockTokens * kBlockExperts;
+}
 
 namespace {
 template <bool EXACT>
@@ -1018,7 +1023,7 @@ moe_status launch_route_scored(const void* u, const void* E, moe_dtype dt, const
     if (st != MOE_OK) return st;
     // a sigmoid needs no other logit: only softmax tokens can ask for all of them
     const bool full = score == MOE_SCORE_SOFTMAX;
-    if (T <= kBlockTokens) {
+    if (blocks_route(T, N_r)) {
       st = launch_router_token<false>(u, E, P, L.S, L.ld, b, T, d, r, idx, gate, counts, logits, rc,
                                       true, T, s);
       return st == MOE_OK && full ? launch_router_full(u, E, b, d, r, idx, gate, counts, rc, s) : st;
