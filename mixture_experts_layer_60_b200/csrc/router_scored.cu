@@ -31,29 +31,28 @@ using namespace sm100;
 // A CTA pair (cta_group::2) owns 256 tokens x Nt <= 256 experts x one slice of
 // d: each CTA stages its 128 token rows (the MMA's M side) and half of the
 // experts, so the pair streams each centroid byte once.  The token side is
-// read once from memory.  T 8192, d 7168, 256 experts: 41 us, u at 2.9 TB/s.
+// read once from memory.  T 8192, d 7168, 256 experts: 54 us, u at 2.2 TB/s.
 // Some 9 us of it are there at any size (TMEM and barriers 1, first loads 1.5
-// to 2.5, last products and drain 1.5, stores 3, exit 1); the rest grows by 640
-// cycles a block of 64 columns, which is u's copy by the 64 pairs that 32
-// tiles of tokens in two slices keep busy.
+// to 2.5, last products and drain 1.5, stores 3, exit 1).
 //
 // The tensor core adds into its accumulator with truncation, and what a step
 // loses follows the largest of its products and running sums, not the logit.
-// The sum is therefore cut every kChunk blocks (16 accumulation steps): two TMEM
+// The sum is therefore cut every kChunk blocks (8 accumulation steps): two TMEM
 // buffers take turns, and the epilogue warps add each finished chunk into float32
 // registers (round to nearest) while the next one runs.  A buffer's round trip
-// through the pair's barriers is some 4000 cycles, so shorter chunks stall the
-// products: chunks of 2, 4, 6 and 8 blocks take 52, 41, 39 and 38 us.
+// through the pair's barriers stalls the products of short chunks (chunks of 2, 4,
+// 6 and 8 blocks take 54, 41, 39 and 38 us), but the error bound, and with it the
+// tokens that are decided again, grows with the chunk: the whole call takes 117 us
+// with 2 and 120 with 4.
 //
 // |u| |E| bounds every product and running sum, and with it the logits' error
 // (logit_error in router_select.cuh).  Two warps sum the tokens' squares from each
-// stage in shared memory once its products are done (5 us of the 41); then it is
-// free.  The experts' are summed by the epilogue warps from global memory before
+// stage in shared memory once its products are done (5 us); then it is free.  The experts' are summed by the epilogue warps from global memory before
 // the first products are done.
 constexpr int BK = 64;                 // bf16 K elements per 128-byte swizzle row
 constexpr int TM = 128;                // token rows per CTA (TMEM lanes)
 constexpr int kMaxN = 256;
-constexpr int kChunk = 4;
+constexpr int kChunk = 2;
 constexpr int STAGES = 6;              // of a block each
 constexpr int kEpiWarps = 16;          // four per TMEM lane quarter, 16-column pieces in turn
 constexpr int kSqWarps = 2;            // square sums

@@ -73,12 +73,12 @@ struct SelectRule {
 // of the largest expert's values.  A step of 16 products cuts each of them at
 // 2^-25 and its sum at 2^-23 of the step's largest product or running sum A (a
 // model, fitted to large values held over chains of small ones): at most 6e-7 A.
-// A chunk sums 16 steps from zero, and a sum that is large and then cancels has
-// A <= |u| |E| / 2 over the chunk's columns, which summed over the chunks is at
-// most |u| |E| / 2 of the whole rows: 4.8e-6 |u| |E|, and the chunks' sums round
-// as they join.  Rows made for it were measured to reach 2.8e-6 (cuts of half on
-// average), N(0,1) rows 6e-8.  (A bound that follows the logits instead lists
-// fewer of those and is wrong where large products cancel.)
+// A chunk sums 8 steps from zero, with A <= |u| |E| over the chunk's columns, which
+// summed over the chunks is at most |u| |E| of the whole rows: 4.8e-6 |u| |E|.  (A
+// sum that is large across the chunks loses at most half a step at each join
+// instead, 4e-6 over 16384 columns.)  Rows made for it reach 3.7e-6, N(0,1) rows
+// 6e-8.  A bound that follows the logits instead lists fewer of those and is wrong
+// where large products cancel.
 constexpr float kLogitError = 5e-6f;
 // Past this the scores' error is no longer their slope's: every logit is made exact.
 constexpr float kWideError = 0.25f;

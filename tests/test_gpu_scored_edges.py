@@ -167,6 +167,15 @@ def _cancelling(kind, T, d, N, seed):
         sign = 1 - 2.0 * (torch.arange(d, device="cuda") // 256 % 2)
         mag = 1 + 0.1 * torch.randn(N, d, generator=g, device="cuda")
         E = (sign * mag * d ** -0.5).to(BF)
+    elif kind == "cuts":
+        # values of about 1 that cancel from chunk to chunk; every other product lies below what
+        # a float32 sum of that size keeps, and their sum tells the experts apart
+        c = torch.arange(0, d, 256, device="cuda")[:d // 512 * 2]
+        u[:] = 2.0 ** -12
+        E[:] = (2.0 ** -13 * (0.5 + torch.randperm(N, device="cuda")[:, None] / N)).to(BF)
+        E[:, c] = 1.0
+        u[:, c[0::2]], u[:, c[1::2]] = 1.0078125, -1.0078125
+        b = None
     elif kind == "vanish":
         # every float32 logit is 0, the exact ones are not: the small term meets a large sum
         e = E[:, 2].clone()
@@ -179,7 +188,7 @@ def _cancelling(kind, T, d, N, seed):
 
 
 KINDS = ["pair_64_3_4", "pair_64_0_511", "pair_256_5_-3", "pair_4096_0_1", "pair_4096_16_200",
-         "mean", "outliers", "coherent", "vanish"]
+         "mean", "outliers", "coherent", "cuts", "vanish"]
 
 
 @pytest.mark.parametrize("T", [300, 1500])
