@@ -329,7 +329,7 @@ moe_status launch_wgrad_pair(const void* A, int M, const void* B, int N, const i
   CUtensorMap tmA, tmB, tmC;
   moe_status st = make_tmap_2d(&tmA, A, bf, 2, M, rows, 64, BK);
   if (st == MOE_OK) st = make_tmap_2d(&tmB, B, bf, 2, N, rows, 64, BK);
-  if (st == MOE_OK) st = 
+  if (st == MOE_OK)
     st = make_tmap_2d_swz(&tmC, C, bf, 2, N, (uint64_t)G * M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (st != MOE_OK) return st;
   static bool attr_done[kMaxSmemDevices] = {};
