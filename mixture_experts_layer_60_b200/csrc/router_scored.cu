@@ -47,8 +47,9 @@ using namespace sm100;
 //
 // |u| |E| bounds every product and running sum, and with it the logits' error
 // (logit_error in router_select.cuh).  Two warps sum the tokens' squares from each
-// stage in shared memory once its products are done (5 us); then it is free.  The experts' are summed by the epilogue warps from global memory before
-// the first products are done.
+// stage in shared memory once its products are done (5 us); then it is free.  The
+// experts' are summed by the epilogue warps from global memory before the first
+// products are done.
 constexpr int BK = 64;                 // bf16 K elements per 128-byte swizzle row
 constexpr int TM = 128;                // token rows per CTA (TMEM lanes)
 constexpr int kMaxN = 256;
@@ -674,8 +675,7 @@ __global__ void __launch_bounds__(128, V <= 8 ? 7 : 1) router_select_kernel(
 // Latency-bound (at T 8192 some 700 tokens are listed), so a thread has two
 // vectors of every row in flight at once (one where a block has more threads
 // than 256); four of them, or more registers than let three blocks share an
-// SM, cost more tokens what they save few: T 1024 55 us, T 256 26 against 36
-// and 23.
+// SM, were slower at T 256 and at T 1024.
 constexpr int kDots = 4;
 template <bool EXACT, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) router_token_kernel(
