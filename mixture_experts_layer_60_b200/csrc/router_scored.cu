@@ -615,7 +615,7 @@ __device__ __forceinline__ void join_slices(const float* __restrict__ row, int S
 }
 
 template <int V>
-__global__ void __launch_bounds__(128, V <= 8 ? 7 : 1) router_select_kernel(
+__global__ void __launch_bounds__(128, V <= 8 ? 7 : V <= 16 ? 4 : 2) router_select_kernel(
     const float* __restrict__ P, int S, int ld, const float* __restrict__ bias, int T,
     SelectRule r, int32_t* __restrict__ idx, float* __restrict__ gate,
     int32_t* __restrict__ counts, float* __restrict__ logits, Recheck rc) {
@@ -628,6 +628,17 @@ __global__ void __launch_bounds__(128, V <= 8 ? 7 : 1) router_select_kernel(
   pdl_wait();
   pdl_trigger();
   const float e2 = largest_e2(rc);
+  float b_lo = 0.f, b_hi = 0.f;
+  if (bias) {
+    b_lo = INFINITY;
+    b_hi = -INFINITY;
+    for (int i = lane; i < N; i += 32) {
+      b_lo = fminf(b_lo, bias[i]);
+      b_hi = fmaxf(b_hi, bias[i]);
+    }
+    b_lo = -sel_warp_max(-b_lo);
+    b_hi = sel_warp_max(b_hi);
+  }
   for (int t = blockIdx.x * wpb + warp; t < T; t += gridDim.x * wpb) {
     float x[V], sc[V], key[V];
     const float logit_err = token_error(rc, S, T, t, e2);
@@ -639,7 +650,9 @@ __global__ void __launch_bounds__(128, V <= 8 ? 7 : 1) router_select_kernel(
         if (j * 32 + lane < N) logits[(size_t)t * N + j * 32 + lane] = x[j];
     }
     int32_t* ti = idx + (size_t)t * r.K;
-    const TokenScale ts = select_keys<V>(x, bias, r, logit_err, sc, key);
+    TokenScale ts = select_keys<V>(x, bias, r, logit_err, sc, key);
+    ts.b_lo = b_lo;
+    ts.b_hi = b_hi;
     const Selection sel = select_core<V>(key, ts, bias, r, wk, ti);
     if (sel.open || wide) {
       int slot = 0;
@@ -649,10 +662,12 @@ __global__ void __launch_bounds__(128, V <= 8 ? 7 : 1) router_select_kernel(
       }
       slot = __shfl_sync(0xffffffffu, slot, 0);
       uint32_t mask = sel.mask;
+      const float most = ts.range_error(sel.lo - key_error(ts.top, sel.lo),
+                                        sel.hi + key_error(ts.top, sel.hi));
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if (j * 32 + lane < N &&
-            (wide || takes_part(key[j], key_error(ts.top, key[j]), sel.lo, sel.hi)))
+            (wide || takes_part(key[j], key_error(most, key[j]), sel.lo, sel.hi)))
           mask |= 1u << j;
       rc.mask[(size_t)slot * 32 + lane] = mask;
       continue;                                     // its gates and load come with the exact pass

@@ -98,19 +98,29 @@ __device__ __forceinline__ float logit_error(float u2, float e2) {
 struct TokenScale {
   float m, z, slope, flat, top;
   bool whole;                    // slope s
+  float b_lo, b_hi;              // least and largest bias
   __device__ __forceinline__ float score_error(float s) const {
     return fmaf(slope, whole ? s : s * (1.f - s), flat);
+  }
+  // Of any expert whose key lies between lo and hi (so its score between lo - b_hi
+  // and hi - b_lo).
+  __device__ __forceinline__ float range_error(float lo, float hi) const {
+    const float s0 = lo - b_hi, s1 = hi - b_lo;
+    const float s = s0 > 0.5f ? fminf(s0, 1.f) : s1 < 0.5f ? fmaxf(s1, 0.f) : 0.5f;
+    return whole ? fminf(top, fmaf(slope, s1, flat)) : fminf(top, fmaf(slope, s * (1.f - s), flat));
   }
 };
 constexpr float kKeyRounding = 1.2e-7f;
 __device__ __forceinline__ TokenScale exact_scale() {
-  return TokenScale{0.f, 1.f, 0.f, 0.f, 0.f, true};
+  return TokenScale{0.f, 1.f, 0.f, 0.f, 0.f, true, 0.f, 0.f};
 }
 // The slope for logits off by at most dx <= kWideError, over which a score's own
 // slope grows by at most e^(4 dx) <= 1 + 8 dx.
 __device__ __forceinline__ float error_slope(float dx, bool softmax, bool bias) {
   return dx * fmaf(8.f, dx, 1.f) * (softmax && bias ? 2.f : 1.f);
 }
+// What float32 functions may lose of a score below the normal range.
+constexpr float kFloor = 2.4e-38f;
 // A key's whole error (an infinite key has none).
 __device__ __forceinline__ float key_error(float score_error, float key) {
   return fabsf(key) < INFINITY ? fmaf(kKeyRounding, fabsf(key), score_error) : 0.f;
@@ -177,7 +187,7 @@ __device__ __forceinline__ TokenScale select_keys(const float (&x)[V], const flo
   w = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(w)));
   s = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s)));
   ts.slope = error_slope(fminf(logit_err, kWideError), softmax, bias != nullptr);
-  ts.flat = 9.6e-7f * s;
+  ts.flat = fmaf(9.6e-7f, s, kFloor);
   ts.top = fmaf(ts.slope, w, ts.flat);
   return ts;
 }
@@ -206,7 +216,9 @@ __device__ __forceinline__ float group_rounding(float a, float b) {
 }
 
 // key: this lane's keys, off by what ts says.  wk: N_r floats of shared memory for
-// this warp.
+// this warp.  A decision is first held against the largest error of all (ts.top);
+// where that leaves it open, against the largest of the keys that it is among
+// (saturated scores have next to none).
 template <int V>
 __device__ __forceinline__ Selection select_core(const float (&key)[V], const TokenScale& ts,
                                                  const float* bias, const SelectRule& r, float* wk,
@@ -288,14 +300,23 @@ __device__ __forceinline__ Selection select_core(const float (&key)[V], const To
       }
     }
     if (out.open) {
+      // the groups near the border, and the last keys that their scores count
+      const float wide = 4.f * (r.group_top * err + grel);
+      float need = gsc >= next - wide && gsc <= last + wide ? sel_val(two ? gb : ga) : INFINITY;
+      // the largest error of the experts that can enter those scores
+      const bool near = need < INFINITY;
+      const float low = -sel_warp_max(near ? -need : -INFINITY);
+      const float high = sel_warp_max(near ? sel_val(ga) : -INFINITY);
+      const float own = ts.range_error(low - 2.f * err - 2.f * rel * fabsf(low), high);
+      out.open = last - next < 2.f * (r.group_top * own + grel);
       // the members that can enter the scores of the groups near the border
-      const float room = 4.f * (r.group_top * err + grel);
-      const float need = gsc >= next - room && gsc <= last + room ? sel_val(two ? gb : ga) : INFINITY;
+      const float room = 4.f * (r.group_top * own + grel);
+      if (!out.open || !(gsc >= next - room && gsc <= last + room)) need = INFINITY;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const uint32_t e = j * 32 + lane, g = e < (uint32_t)N ? e * inv_gs >> 22 : 0u;
         const float want = __shfl_sync(0xffffffffu, need, g);
-        if (e < (uint32_t)N && key[j] >= want - 2.f * err - 2.f * rel * fabsf(want))
+        if (e < (uint32_t)N && key[j] >= want - 2.f * own - 2.f * rel * fabsf(want))
           out.mask |= 1u << j;
       }
     }
@@ -359,6 +380,10 @@ __device__ __forceinline__ Selection select_core(const float (&key)[V], const To
     if (n <= r.K) rest = -INFINITY;
     const float last_lo = __shfl_sync(0xffffffffu, lo, r.K - 1);
     const float last_hi = __shfl_sync(0xffffffffu, hi, r.K - 1);
+    if (rest > last_lo) {
+      const float next = __shfl_sync(0xffffffffu, won, r.K & 31);
+      rest = next + key_error(ts.range_error(last_lo - key_error(err, last_lo), next), next);
+    }
     if (rest > last_lo) {
       out.lo = fminf(out.lo, last_lo);
       out.hi = fmaxf(out.hi, last_hi);
@@ -496,8 +521,8 @@ __device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRul
                                             int32_t* __restrict__ counts) {
   __shared__ double red_z[32];
   __shared__ uint32_t red_m[32], red_w[32], red_s[32];
-  __shared__ float gkey[32][2];
-  __shared__ unsigned s_near;
+  __shared__ float gkey[32][2], gneed[32];
+  __shared__ uint32_t gerr[32];        // the largest error of the inexact keys near a group's score
   __shared__ int n_list;
   __shared__ uint32_t s_lo, s_hi;      // the keys, in order form, between which open pairs lie
   const int e = threadIdx.x, N = r.N_r, K = r.K, lane = e & 31;
@@ -533,7 +558,7 @@ __device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRul
           block_max(__float_as_uint(fmaxf(0.f, ts.whole ? s : s * (1.f - s))), red_w));
       smax = __uint_as_float(block_max(__float_as_uint(fmaxf(0.f, s)), red_s));
       ts.slope = error_slope(logit_err, softmax, bias != nullptr);
-      ts.flat = 4.8e-7f * smax;
+      ts.flat = fmaf(4.8e-7f, smax, kFloor);
       ts.top = fmaf(ts.slope, w, ts.flat);
       eta = softmax ? logit_err : 0.f;
       if (mine && !ex) ke = key_error(ts.score_error(s), key);
@@ -542,8 +567,8 @@ __device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRul
     const float err = ts.top, rel = err > 0.f ? kKeyRounding : 0.f;
     uint32_t o = mine ? sel_ord(key) : 0u;
     if (mine) b.ord[e] = o;
-    if (e == 0) { n_list = 0; s_lo = 0xffffffffu; s_hi = 0u; s_near = 0u; }
-    if (e < 32) gkey[e][0] = gkey[e][1] = 0.f;
+    if (e == 0) { n_list = 0; s_lo = 0xffffffffu; s_hi = 0u; }
+    if (e < 32) { gkey[e][0] = gkey[e][1] = gneed[e] = 0.f; gerr[e] = 0u; }
     __syncthreads();
     bool want = false, z_open = false;
     if (grouped) {
@@ -564,19 +589,23 @@ __device__ __forceinline__ bool block_route(const BlockRoute& b, const SelectRul
           place += v > o || (v == o && i < e);
         }
       }
+      // gneed: what the last key that the group's score counts is at least
       if (mine && place < 2) gkey[g][place] = key;
+      if (mine && place == (two ? 1 : 0)) gneed[g] = key - ke;
       __syncthreads();
-      const float need = gkey[g][two ? 1 : 0];       // the last key the group's score counts
-      const bool near = mine && !ex && key >= need - 2.f * err - 2.f * rel * fabsf(need);
-      if (near) atomicOr(&s_near, 1u << g);
+      const bool near = mine && !ex && key + ke >= gneed[g];
+      if (near) atomicMax(&gerr[g], __float_as_uint(ke));
       __syncthreads();
       // groups: lane q of every warp holds group q
       const bool has = lane < r.n_groups;
       const float gsc = has ? (two ? gkey[lane][0] + gkey[lane][1] : gkey[lane][0]) : 0.f;
       const uint32_t go = has ? sel_ord(gsc) : 0u;
-      const float ge = has && ((s_near >> lane) & 1u)
-                           ? r.group_top * err + rel * group_rounding(gkey[lane][0], two ? gkey[lane][1] : 0.f)
-                           : 0.f;
+      // a score with an inexact key near it: that error for each key it counts (an exact
+      // one among them has less), and the sum's rounding
+      const float gmax = has ? __uint_as_float(gerr[lane]) : 0.f;
+      const float ge = gmax > 0.f ? r.group_top * gmax +
+                                        rel * group_rounding(gkey[lane][0], two ? gkey[lane][1] : 0.f)
+                                  : 0.f;
       int before = 0;
       for (int q = 0; q < r.n_groups; ++q) {
         const uint32_t v = __shfl_sync(0xffffffffu, go, q);

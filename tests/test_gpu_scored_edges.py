@@ -265,6 +265,28 @@ def test_special_rows_route_as_few_tokens_do(T, score):
         assert ((gate[:8] - g).abs()[~nan] <= 4e-4 * g.abs()[~nan] + 1e-30).all()
 
 
+@pytest.mark.parametrize("T", [5, 300, 1300])
+def test_selection_among_scores_below_the_normal_range(T):
+    """Sigmoids of logits near -95 are subnormal floats: a rounding of each still orders them."""
+    u, E, _ = _normal(T, 512, 64, 47)
+    u[:, 0] = 1.0
+    E[:, 0] = -95.0
+    _check_selection(u, E, None, 6, SIG)
+    _check_selection(u, E, None, 6, SIG, n_groups=8, topk_groups=4, group_top=2)
+
+
+@pytest.mark.parametrize("T", [300, 1300])
+@pytest.mark.parametrize("scale", [4, 16, 64])
+def test_selection_of_saturated_scores(T, scale):
+    """Logits of many standard deviations: scores a few float32 steps below 1, and ties at 1."""
+    for N, d, K in ((256, 1024, 8), (64, 512, 40)):
+        u, E, b = _normal(T, d, N, 53)
+        E = (E.float() * scale).to(BF)
+        for score in (SIG, SOFT):
+            _check_selection(u, E, b, K, score)
+            _check_selection(u, E, None, min(K, 16), score, n_groups=8, topk_groups=4, group_top=2)
+
+
 # ------------------------------------------------------------------ groups
 
 @pytest.mark.parametrize("T", [64, 1300])
